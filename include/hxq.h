@@ -367,6 +367,161 @@ int hxq_linear_info(hxq_linear_t h, int* mode, int* N, int* K, int64_t* n_sideca
 /* Free a handle (NULL is ignored). Synchronises the device first. */
 void hxq_linear_destroy(hxq_linear_t h);
 
+/*
+ * ---- 8-bit-float layers: weights and activations as e4m3 values with a
+ * scale for each block of 128. Checkpoints that keep some layers in 8-bit
+ * float (8 bits per weight, like the scalar mode) have no codebook to decode:
+ * the tensor cores multiply the bytes as they are, in prefill and decode, for
+ * one layer or for the experts of one. The pages have no counterpart.
+ *
+ * Format. A byte is an e4m3 value (sign, 4 exponent bits, 3 significand bits;
+ * largest magnitude 448, no infinities, NaN 0x7f and 0xff). It stands for its
+ * value times the fp32 scale of its block: one row x 128 columns of an
+ * activation, 128 x 128 of a weight matrix; the last block of a row or column
+ * may be partial. Layouts, row-major:
+ *  activation  uint8[M][ld], ld = hxq_fp8_ld(K) = K rounded up to 16; bytes
+ *              past K are written as 0 and never read; scales
+ *              float[M][ceil(K/128)]
+ *  weights     uint8[N][K] and float[ceil(N/128)][ceil(K/128)]; the experts
+ *              of one layer back to back
+ * The products take any fp32 scales. The quantisers below write powers of
+ * two: the smallest s with max |v| <= 448 s over the block, kept in
+ * [2^-126, 2^120], and 1 for a block of zeros. Dividing by such a scale is
+ * exact, so a byte is its value rounded once (to nearest, ties to even). NaN
+ * is left out of the maximum and gives NaN; infinity gives NaN.
+ *
+ * All of these calls are asynchronous on `stream` and take device pointers;
+ * 8-bit activations must be 16-byte aligned, everything else as its elements.
+ * The current device must be the one that holds the memory (and the handle).
+ * Nothing is allocated and no workspace exists, so calls on one handle may
+ * overlap in time on different streams, and any of them may be captured into
+ * a CUDA graph. Outputs must not overlap inputs except where said. Zero rows
+ * are allowed (nothing is launched; their pointers may be NULL).
+ */
+typedef struct hxq_fp8* hxq_fp8_t;
+
+/* Element types of inputs (and of outputs: the values of HXQ_OUT_*). */
+enum {
+    HXQ_TYPE_F32 = 0,
+    HXQ_TYPE_BF16 = 1
+};
+
+/* Most experts in one handle. */
+enum { HXQ_FP8_MAX_EXPERTS = 1024 };
+
+/* Row length in bytes of an 8-bit activation of K columns (K >= 1). */
+int64_t hxq_fp8_ld(int K);
+
+/*
+ * x [rows][cols] (x_type) as an 8-bit activation: q and scales. Returns
+ * HXQ_EINVAL for NULL pointers, an unknown type, rows < 0, cols < 1, 2^31
+ * blocks or more, misaligned pointers, or q not reachable from the current
+ * device; HXQ_ECUDA if the launch fails.
+ */
+int hxq_fp8_quantize(const void* x, int x_type, int64_t rows, int cols, uint8_t* q, float* scales,
+                     void* stream);
+
+/*
+ * The gated activation between an MLP's products, as an 8-bit activation:
+ * gate_up [rows][2 * cols] holds gate in its first cols columns and up in the
+ * others; q and scales [rows][cols] receive gate / (1 + exp(-gate)) * up,
+ * formed in fp32. Errors as hxq_fp8_quantize.
+ */
+int hxq_fp8_swiglu(const void* gate_up, int type, int64_t rows, int cols, uint8_t* q, float* scales,
+                   void* stream);
+
+/*
+ * Weights W [n_experts][N][K] (fp32 or bf16; for instance what hxq_decode
+ * writes) in the layout that hxq_fp8_create reads: q [n_experts][N][K] and
+ * one scale per 128 x 128 block. Returns HXQ_EINVAL for NULL pointers, an
+ * unknown type, sizes < 1, 2^31 blocks or more, or q not reachable from the
+ * current device; HXQ_ECUDA if the launch fails.
+ */
+int hxq_fp8_encode(const void* W, int type, int n_experts, int N, int K, uint8_t* q, float* scales,
+                   void* stream);
+
+/*
+ * The norm in front of a layer, with the residual's addition:
+ *   t = x + residual, added in fp32 and rounded to the residual's type (t = x
+ *       without one)
+ *   h = t / sqrt(mean(t^2) + eps) * weight
+ * per row of [rows][cols].
+ *
+ *  x, x_type      the last layer's output, fp32 or bf16
+ *  residual       of residual_type, or NULL
+ *  sum            receives t (residual_type), or NULL; may be `residual`
+ *                 itself, or x where the types agree
+ *  weight         cols floats, or NULL for ones
+ *  eps            >= 0
+ *  y_bf16         receives h as bf16 (what hxq_linear_forward reads), or NULL
+ *  q, scales      receive h as an 8-bit activation (what hxq_fp8_forward
+ *                 reads; from the fp32 h), or both NULL
+ *
+ * h is formed in fp32; the mean of squares, and every scale that the rounding
+ * of h could decide, in 64 bits. Returns HXQ_EINVAL for a NULL x, neither y
+ * nor q, one of q and scales without the other, a sum without a residual,
+ * unknown types, a negative, infinite or NaN eps, sizes as hxq_fp8_quantize,
+ * misaligned or unreachable outputs; HXQ_ECUDA if the launch fails.
+ */
+int hxq_rmsnorm(const void* x, int x_type, const void* residual, void* sum, int residual_type,
+                const float* weight, float eps, int64_t rows, int cols, void* y_bf16, uint8_t* q,
+                float* scales, void* stream);
+
+/*
+ * Build a handle of 8-bit weights on the current device, of one layer
+ * (n_experts 1) or of the experts of one: W and scales in the layout above,
+ * in device or host memory. The call copies them into tiles of 128 x 128 that
+ * it owns (rows and columns zero padded to whole tiles) and synchronises the
+ * device: the caller may free its buffers afterwards. It needs one expert's
+ * weights as temporary device memory, and cannot be made while a stream is
+ * being captured. The handle is immutable. Returns HXQ_EINVAL for a NULL
+ * pointer, n_experts outside 1..HXQ_FP8_MAX_EXPERTS, N < 1, K < 1 or 2^24
+ * tiles or more; HXQ_EUNSUPPORTED, HXQ_ENOMEM, HXQ_ECUDA as
+ * hxq_linear_create.
+ */
+int hxq_fp8_create(const uint8_t* W, const float* scales, int n_experts, int N, int K, hxq_fp8_t* out);
+
+/*
+ * y[M][N] = x . W^T (+ bias[N], floats, or NULL) for a handle of one layer:
+ *   y[m][n] = sum over blocks b of xs[m][b] * ws[n / 128][b] *
+ *             (sum over k in b of xq[m][k] * wq[n][k])
+ * stored as out_type, rounded to nearest even for HXQ_TYPE_BF16. Products and
+ * sums inside a block run on the tensor cores with fp32 accumulation, the sum
+ * over blocks is fp32: within (64 + K / 128) 2^-24 sum |x||w| of the exact
+ * value before the output's rounding. Results are bitwise repeatable; a row's result does not
+ * depend on the other rows' values.
+ * Returns HXQ_EINVAL for a NULL handle/xq/xs/y, a handle of several experts,
+ * M < 0, an unknown out_type, misaligned pointers, 2^31 output tiles, or
+ * another device current; HXQ_ECUDA if a launch fails.
+ */
+int hxq_fp8_forward(hxq_fp8_t h, const uint8_t* xq, const float* xs, const float* bias, void* y, int out_type,
+                    int M, void* stream);
+
+/*
+ * The products of all experts of a handle in one launch. Rows are sorted by
+ * expert: expert e has the rows [offsets[e], offsets[e + 1]) of xq, xs and y,
+ * offsets being n_experts + 1 int32 values in device memory, not falling, in
+ * 0..M (the host never reads them). An expert may have no rows. Rows before
+ * offsets[0] or from offsets[n_experts] on are not read and their y is left
+ * as it was. bias [n_experts][N] floats or NULL. Numerics and errors as
+ * hxq_fp8_forward (plus NULL offsets). Offsets that break these rules give
+ * unspecified values in y, but nothing outside x and y's M rows is touched.
+ */
+int hxq_fp8_forward_grouped(hxq_fp8_t h, const uint8_t* xq, const float* xs, const int32_t* offsets,
+                            const float* bias, void* y, int out_type, int M, void* stream);
+
+/* Shape of a handle: any output pointer may be NULL. HXQ_EINVAL if h is NULL. */
+int hxq_fp8_info(hxq_fp8_t h, int* n_experts, int* N, int* K);
+
+/*
+ * Synchronise the device and report whether a kernel of this handle gave up a
+ * bounded device-side wait since the last check, as hxq_linear_check.
+ */
+int hxq_fp8_check(hxq_fp8_t h);
+
+/* Free a handle (NULL is ignored). Synchronises the device first. */
+void hxq_fp8_destroy(hxq_fp8_t h);
+
 /* Static description of a status code. */
 const char* hxq_strerror(int code);
 

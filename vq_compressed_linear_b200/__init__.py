@@ -37,6 +37,9 @@ HXQ_KERNEL_TC = 2
 HXQ_OUT_F32 = 0
 HXQ_OUT_BF16 = 1
 HXQ_MAX_GROUP = 4
+HXQ_TYPE_F32 = 0
+HXQ_TYPE_BF16 = 1
+HXQ_FP8_MAX_EXPERTS = 1024
 
 _vp, _i, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64
 lib.hxq_linear_create.argtypes = [_vp, _vp, _i, _vp, _vp, _i64, _i, _i, ctypes.POINTER(_vp)]
@@ -72,6 +75,28 @@ lib.hxq_kmeans.argtypes = [_vp, _i64, _i, _i, _i, _vp, _vp, _vp]
 lib.hxq_kmeans.restype = _i
 lib.hxq_encode.argtypes = [_vp, _i, _i, _i, _vp, ctypes.c_float, _vp, _vp, _vp, _i64, _vp, _vp]
 lib.hxq_encode.restype = _i
+lib.hxq_fp8_ld.argtypes = [_i]
+lib.hxq_fp8_ld.restype = _i64
+lib.hxq_fp8_quantize.argtypes = [_vp, _i, _i64, _i, _vp, _vp, _vp]
+lib.hxq_fp8_quantize.restype = _i
+lib.hxq_fp8_swiglu.argtypes = [_vp, _i, _i64, _i, _vp, _vp, _vp]
+lib.hxq_fp8_swiglu.restype = _i
+lib.hxq_fp8_encode.argtypes = [_vp, _i, _i, _i, _i, _vp, _vp, _vp]
+lib.hxq_fp8_encode.restype = _i
+lib.hxq_rmsnorm.argtypes = [_vp, _i, _vp, _vp, _i, _vp, ctypes.c_float, _i64, _i, _vp, _vp, _vp, _vp]
+lib.hxq_rmsnorm.restype = _i
+lib.hxq_fp8_create.argtypes = [_vp, _vp, _i, _i, _i, ctypes.POINTER(_vp)]
+lib.hxq_fp8_create.restype = _i
+lib.hxq_fp8_forward.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, _vp]
+lib.hxq_fp8_forward.restype = _i
+lib.hxq_fp8_forward_grouped.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _vp]
+lib.hxq_fp8_forward_grouped.restype = _i
+lib.hxq_fp8_info.argtypes = [_vp, ctypes.POINTER(_i), ctypes.POINTER(_i), ctypes.POINTER(_i)]
+lib.hxq_fp8_info.restype = _i
+lib.hxq_fp8_check.argtypes = [_vp]
+lib.hxq_fp8_check.restype = _i
+lib.hxq_fp8_destroy.argtypes = [_vp]
+lib.hxq_fp8_destroy.restype = None
 lib.hxq_linear_destroy.argtypes = [_vp]
 lib.hxq_linear_destroy.restype = None
 lib.hxq_strerror.argtypes = [_i]
@@ -80,6 +105,8 @@ lib.hxq_strerror.restype = ctypes.c_char_p
 EXPORTED = ("hxq_linear_create", "hxq_linear_forward", "hxq_linear_forward_ex", "hxq_linear_forward_out",
             "hxq_linear_forward_host", "hxq_linear_forward_noalloc", "hxq_group_create", "hxq_group_forward", "hxq_group_destroy", "hxq_assign", "hxq_kmeans", "hxq_encode", "hxq_decode",
             "hxq_linear_check", "hxq_test_forward_withheld", "hxq_linear_info", "hxq_linear_destroy",
+            "hxq_fp8_ld", "hxq_fp8_quantize", "hxq_fp8_swiglu", "hxq_fp8_encode", "hxq_rmsnorm", "hxq_fp8_create",
+            "hxq_fp8_forward", "hxq_fp8_forward_grouped", "hxq_fp8_info", "hxq_fp8_check", "hxq_fp8_destroy",
             "hxq_strerror")
 
 
@@ -215,6 +242,64 @@ def hxq_linear_info(h) -> tuple[int, int, int, int]:
 
 def hxq_linear_destroy(h) -> None:
     lib.hxq_linear_destroy(h)
+
+
+def hxq_fp8_ld(K) -> int:
+    return lib.hxq_fp8_ld(int(K))
+
+
+def hxq_fp8_quantize(x, x_type, rows, cols, q, scales, stream=None) -> None:
+    _check(lib.hxq_fp8_quantize(_ptr(x), int(x_type), int(rows), int(cols), _ptr(q), _ptr(scales), _stream(stream)),
+           "hxq_fp8_quantize")
+
+
+def hxq_fp8_swiglu(gate_up, type, rows, cols, q, scales, stream=None) -> None:
+    _check(lib.hxq_fp8_swiglu(_ptr(gate_up), int(type), int(rows), int(cols), _ptr(q), _ptr(scales),
+                              _stream(stream)), "hxq_fp8_swiglu")
+
+
+def hxq_fp8_encode(W, type, n_experts, N, K, q, scales, stream=None) -> None:
+    _check(lib.hxq_fp8_encode(_ptr(W), int(type), int(n_experts), int(N), int(K), _ptr(q), _ptr(scales),
+                              _stream(stream)), "hxq_fp8_encode")
+
+
+def hxq_rmsnorm(x, x_type, residual, sum, residual_type, weight, eps, rows, cols, y_bf16, q, scales,
+                stream=None) -> None:
+    _check(lib.hxq_rmsnorm(_ptr(x), int(x_type), _ptr(residual), _ptr(sum), int(residual_type), _ptr(weight),
+                           float(eps), int(rows), int(cols), _ptr(y_bf16), _ptr(q), _ptr(scales), _stream(stream)),
+           "hxq_rmsnorm")
+
+
+def hxq_fp8_create(W, scales, n_experts, N, K) -> int:
+    """Returns the handle (an integer); raises HXQError on failure."""
+    h = _vp()
+    _check(lib.hxq_fp8_create(_ptr(W), _ptr(scales), int(n_experts), int(N), int(K), ctypes.byref(h)),
+           "hxq_fp8_create")
+    return h.value
+
+
+def hxq_fp8_forward(h, xq, xs, bias, y, out_type, M, stream=None) -> None:
+    _check(lib.hxq_fp8_forward(h, _ptr(xq), _ptr(xs), _ptr(bias), _ptr(y), int(out_type), int(M), _stream(stream)),
+           "hxq_fp8_forward")
+
+
+def hxq_fp8_forward_grouped(h, xq, xs, offsets, bias, y, out_type, M, stream=None) -> None:
+    _check(lib.hxq_fp8_forward_grouped(h, _ptr(xq), _ptr(xs), _ptr(offsets), _ptr(bias), _ptr(y), int(out_type),
+                                       int(M), _stream(stream)), "hxq_fp8_forward_grouped")
+
+
+def hxq_fp8_info(h) -> tuple[int, int, int]:
+    e, n, k = _i(), _i(), _i()
+    _check(lib.hxq_fp8_info(h, ctypes.byref(e), ctypes.byref(n), ctypes.byref(k)), "hxq_fp8_info")
+    return e.value, n.value, k.value
+
+
+def hxq_fp8_check(h) -> None:
+    _check(lib.hxq_fp8_check(h), "hxq_fp8_check")
+
+
+def hxq_fp8_destroy(h) -> None:
+    lib.hxq_fp8_destroy(h)
 
 
 # ---- convenience wrapper -----------------------------------------------------
@@ -363,3 +448,196 @@ def encode(W, mode, codebook, threshold, max_sidecar=None, stream=None):
             m = min(n, cap)
             return idx, pos[:m], val[:m]
         cap = n
+
+
+# ---- 8-bit-float layers --------------------------------------------------------
+# Tensors are checked here for what the C ABI cannot see: shape, type,
+# contiguity and device. A mismatch raises HXQError with HXQ_EINVAL.
+
+def _want(cond, what: str) -> None:
+    if not cond:
+        raise HXQError(HXQ_EINVAL, what)
+
+
+_types: dict = {}
+
+
+def _fp8_types() -> dict:
+    """torch dtype -> HXQ_TYPE_*, and the 8-bit dtypes (filled at first use:
+    importing this module does not import torch)."""
+    if not _types:
+        import torch
+        _types.update({torch.float32: HXQ_TYPE_F32, torch.bfloat16: HXQ_TYPE_BF16, "f32": torch.float32,
+                       "bf16": torch.bfloat16, "q": torch.float8_e4m3fn, "q8": (torch.float8_e4m3fn, torch.uint8),
+                       "i32": torch.int32, "empty": torch.empty, "device": torch.cuda.current_device})
+    return _types
+
+
+def _input(t, what: str):
+    """A 2D CUDA tensor of float32 or bfloat16 on the current device, contiguous; its HXQ_TYPE_*."""
+    ty = _fp8_types()
+    code = ty.get(t.dtype)
+    _want(code is not None and t.is_cuda and t.dim() >= 1 and t.shape[-1] > 0 and t.get_device() == ty["device"](),
+          f"{what}: a float32 or bfloat16 tensor on the current CUDA device")
+    return t if t.is_contiguous() else t.contiguous(), code
+
+
+def _output(t, shape, dtypes, device, what: str):
+    """`t`, checked, or a new tensor of that shape (of the first dtype)."""
+    if t is None:
+        return _fp8_types()["empty"](shape, dtype=dtypes[0], device=device)
+    _want(t.shape == shape and t.dtype in dtypes and t.is_contiguous() and t.device == device,
+          f"{what}: a contiguous {dtypes[0]} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _quantized(rows, cols, q, scales, device, what):
+    ty = _fp8_types()
+    return (_output(q, (rows, (cols + 15) // 16 * 16), ty["q8"], device, what + ": q"),
+            _output(scales, (rows, (cols + 127) // 128), (ty["f32"],), device, what + ": scales"))
+
+
+def fp8_quantize(x, q=None, scales=None, stream=None):
+    """x [M, K] (float32 or bfloat16 CUDA) as an 8-bit activation. Returns
+    (q float8_e4m3fn [M, K rounded up to 16], scales float32 [M, ceil(K / 128)])."""
+    x, code = _input(x, "fp8_quantize")
+    _want(x.dim() == 2, "fp8_quantize: x is [M, K]")
+    rows, cols = x.shape
+    q, scales = _quantized(rows, cols, q, scales, x.device, "fp8_quantize")
+    hxq_fp8_quantize(x, code, rows, cols, q, scales, stream)
+    return q, scales
+
+
+def fp8_swiglu(gate_up, q=None, scales=None, stream=None):
+    """silu(gate) * up of gate_up [M, 2 K] (gate first) as an 8-bit
+    activation [M, K]; returns (q, scales) as fp8_quantize."""
+    x, code = _input(gate_up, "fp8_swiglu")
+    _want(x.dim() == 2 and x.shape[1] % 2 == 0, "fp8_swiglu: gate_up is [M, 2 K]")
+    rows, cols = x.shape[0], x.shape[1] // 2
+    q, scales = _quantized(rows, cols, q, scales, x.device, "fp8_swiglu")
+    hxq_fp8_swiglu(x, code, rows, cols, q, scales, stream)
+    return q, scales
+
+
+def fp8_encode(W, q=None, scales=None, stream=None):
+    """Weights [N, K] or [E, N, K] (float32 or bfloat16 CUDA) as 8-bit values
+    of the same shape and scales [(E,) ceil(N / 128), ceil(K / 128)]: what
+    Fp8Linear takes."""
+    W, code = _input(W, "fp8_encode")
+    _want(W.dim() in (2, 3) and W.numel() > 0, "fp8_encode: W is [N, K] or [E, N, K]")
+    ty = _fp8_types()
+    N, K = W.shape[-2:]
+    q = _output(q, W.shape, ty["q8"], W.device, "fp8_encode: q")
+    scales = _output(scales, (*W.shape[:-2], (N + 127) // 128, (K + 127) // 128), (ty["f32"],), W.device,
+                     "fp8_encode: scales")
+    hxq_fp8_encode(W, code, W.shape[0] if W.dim() == 3 else 1, N, K, q, scales, stream)
+    return q, scales
+
+
+def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=None, scales=None, want=None,
+            stream=None):
+    """t = x + residual (rounded to the residual's type), then
+    h = t / sqrt(mean(t^2) + eps) * weight per row of x [M, K].
+
+    want: "q" for h as an 8-bit activation (what Fp8Linear takes), "y" for h
+    as bfloat16 (what HelixLinear takes), "qy" for both; by default what is
+    given of y and q (q if neither is). sum_out receives t (it may be the
+    residual itself; a new tensor if there is a residual and none is given).
+    Returns (q, scales, y, sum), None for what was not asked for."""
+    x, xt = _input(x, "rmsnorm")
+    _want(x.dim() == 2, "rmsnorm: x is [M, K]")
+    ty = _fp8_types()
+    rows, cols = x.shape
+    dev = x.device
+    if want is None:
+        want = ("q" if q is not None or y is None else "") + ("y" if y is not None else "")
+    _want(want in ("q", "y", "qy", "yq"), "rmsnorm: want is 'q', 'y' or 'qy'")
+    rt = xt
+    if residual is not None:
+        residual, rt = _input(residual, "rmsnorm: residual")
+        _want(residual.shape == x.shape and residual.device == dev, "rmsnorm: residual has the shape of x")
+        sum_out = _output(sum_out, x.shape, (residual.dtype,), dev, "rmsnorm: sum_out")
+    else:
+        _want(sum_out is None, "rmsnorm: sum_out without a residual")
+    if weight is not None:
+        _output(weight, (cols,), (ty["f32"],), dev, "rmsnorm: weight")
+    if "q" in want:
+        q, scales = _quantized(rows, cols, q, scales, dev, "rmsnorm")
+    else:
+        _want(q is None and scales is None, "rmsnorm: q without 'q' in want")
+    if "y" in want:
+        y = _output(y, x.shape, (ty["bf16"],), dev, "rmsnorm: y")
+    else:
+        _want(y is None, "rmsnorm: y without 'y' in want")
+    hxq_rmsnorm(x, xt, residual, sum_out, rt, weight, eps, rows, cols, y, q, scales, stream)
+    return q, scales, y, sum_out
+
+
+class Fp8Linear:
+    """8-bit-float weights owned by libhxq: of one layer (W [N, K], scales
+    [ceil(N / 128), ceil(K / 128)]) or of the experts of one ([E, N, K] and
+    [E, ...]), host or device tensors; the handle copies them. Activations
+    come as the pair that fp8_quantize, fp8_swiglu and rmsnorm return.
+    """
+
+    def __init__(self, W, scales):
+        ty = _fp8_types()
+        _want(W.dim() in (2, 3) and W.numel() > 0 and W.dtype in ty["q8"], "Fp8Linear: W is [N, K] or [E, N, K], 8 bits")
+        self.grouped = W.dim() == 3
+        self.E = int(W.shape[0]) if self.grouped else 1
+        self.N, self.K = int(W.shape[-2]), int(W.shape[-1])
+        self._ld, self._kb = (self.K + 15) // 16 * 16, (self.K + 127) // 128
+        _want(scales.dtype == ty["f32"] and scales.shape == (*W.shape[:-2], (self.N + 127) // 128, self._kb),
+              "Fp8Linear: scales are float32, one per 128 x 128 block")
+        self.handle = hxq_fp8_create(W.contiguous(), scales.contiguous(), self.E, self.N, self.K)
+
+    @classmethod
+    def from_weight(cls, W) -> "Fp8Linear":
+        """From float32 or bfloat16 CUDA weights [N, K] or [E, N, K]."""
+        return cls(*fp8_encode(W))
+
+    def _run(self, xq, xs, offsets, bias, out_dtype, y, stream):
+        ty = _fp8_types()
+        M, dev = xq.shape[0], xq.device
+        _want(xq.shape == (M, self._ld) and xq.dtype in ty["q8"] and xq.is_contiguous() and
+              dev.index == ty["device"](), f"Fp8Linear: xq is a contiguous 8-bit tensor [M, {self._ld}] on the current "
+              "CUDA device")
+        _output(xs, (M, self._kb), (ty["f32"],), dev, "Fp8Linear: xs")
+        if bias is not None:
+            _output(bias, (self.E, self.N) if self.grouped else (self.N,), (ty["f32"],), dev, "Fp8Linear: bias")
+        y = _output(y, (M, self.N), (ty["bf16" if out_dtype == HXQ_OUT_BF16 else "f32"],), dev, "Fp8Linear: y")
+        if offsets is None:
+            hxq_fp8_forward(self.handle, xq, xs, bias, y, out_dtype, M, stream)
+        else:
+            _output(offsets, (self.E + 1,), (ty["i32"],), dev, "Fp8Linear: offsets")
+            hxq_fp8_forward_grouped(self.handle, xq, xs, offsets, bias, y, out_dtype, M, stream)
+        return y
+
+    def forward(self, xq, xs, bias=None, out_dtype=HXQ_OUT_F32, y=None, stream=None):
+        """y = x . W^T (+ bias [N]) as float32, or as bfloat16 with
+        out_dtype=HXQ_OUT_BF16."""
+        _want(not self.grouped, "Fp8Linear: forward_grouped runs the experts")
+        return self._run(xq, xs, None, bias, out_dtype, y, stream)
+
+    __call__ = forward
+
+    def forward_grouped(self, xq, xs, offsets, bias=None, out_dtype=HXQ_OUT_F32, y=None, stream=None):
+        """Rows offsets[e] .. offsets[e + 1] - 1 (int32 CUDA [E + 1]) times
+        expert e's weights (+ bias [E, N]). Rows outside all of them are left
+        as they were in y (unwritten in a new y)."""
+        _want(self.grouped and offsets is not None, "Fp8Linear: forward_grouped takes weights [E, N, K] and offsets")
+        return self._run(xq, xs, offsets, bias, out_dtype, y, stream)
+
+    def check(self) -> None:
+        hxq_fp8_check(self.handle)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            hxq_fp8_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
