@@ -27,6 +27,10 @@
 
 #include <algorithm>
 #include <climits>
+#include <memory>
+#include <mutex>
+#include <new>
+#include <vector>
 
 #include "hxq_fp8.cuh"
 
@@ -78,27 +82,57 @@ __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
                ::"r"(map_to_rank(smem_u32(bar), rank)) : "memory");
 }
-// mbar_wait for barriers that other CTAs of the cluster arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t i = 0;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((i & 63) == 63) {
+// Waits, bounded at kWaitCycles (about 2 s): false, with *abort set, when the
+// limit passes or another thread of the CTA gave up. The limit is counted in
+// SM cycles: reading %globaltimer costs more than an ordinary wait here takes
+// (measured below).
+constexpr long long kWaitCycles = 4000000000ll;
+
+template <bool CLUSTER>
+__device__ __forceinline__ bool try_bar(uint64_t* bar, uint32_t parity) {
+  if (!CLUSTER) return mbar_try_wait(bar, parity);
+  uint32_t ok;  // for barriers that other CTAs of the cluster arrive on
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (try_bar<CLUSTER>(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (try_bar<CLUSTER>(bar, parity)) return true;
+    if ((i & 31) == 0) {
       if (*abort) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      if (clock64() - t0 > kWaitCycles) {
         *abort = 1;
         return false;
       }
     }
   }
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// wait_bar of a whole warp, which takes the same way afterwards.
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
+}
+
+__device__ __forceinline__ void put_out(const Fp8Out& o, size_t at, float v) {
+  if (o.bf16)
+    static_cast<__nv_bfloat16*>(o.y)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<float*>(o.y)[at] = v;
 }
 
 // ---- row ranges of the experts ------------------------------------------------
@@ -118,56 +152,59 @@ __device__ __forceinline__ Ranges ranges_at(void* p, int E) {
 }
 constexpr size_t ranges_bytes(int E) { return ((size_t)(3 * E + 1) * sizeof(int) + 15) / 16 * 16; }
 
-// All threads of the CTA; ends with a barrier.
-template <int BN>
+// All threads of the CTA; ends with a barrier. Nothing to do for one layer.
+template <int BN, bool GROUPED>
 __device__ __forceinline__ void load_ranges(const Ranges& R, const MmArgs& a) {
-  const int E = a.n_experts;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) {
-    int lo = 0, hi = a.M;
-    if (a.offsets) {
-      lo = min(max(__ldg(a.offsets + e), 0), a.M);
-      hi = min(max(__ldg(a.offsets + e + 1), lo), a.M);
+  if (GROUPED) {
+    const int E = a.n_experts;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      const int lo = min(max(__ldg(a.offsets + e), 0), a.M);
+      R.first[e] = lo;
+      R.rows[e] = min(max(__ldg(a.offsets + e + 1), lo), a.M) - lo;
     }
-    R.first[e] = lo;
-    R.rows[e] = hi - lo;
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + (int)threadIdx.x;
-      const int n = e < E ? (R.rows[e] + BN - 1) / BN : 0;
-      int s = n;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int base = 0;
+      for (int e0 = 0; e0 < E; e0 += 32) {
+        const int e = e0 + (int)threadIdx.x;
+        const int n = e < E ? (R.rows[e] + BN - 1) / BN : 0;
+        int s = n;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, s, o);
-        if ((int)threadIdx.x >= o) s += t;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, s, o);
+          if ((int)threadIdx.x >= o) s += t;
+        }
+        if (e < E) R.unit0[e] = base + s - n;
+        base += __shfl_sync(0xffffffffu, s, 31);
       }
-      if (e < E) R.unit0[e] = base + s - n;
-      base += __shfl_sync(0xffffffffu, s, 31);
+      if (threadIdx.x == 0) R.unit0[E] = base;
     }
-    if (threadIdx.x == 0) R.unit0[E] = base;
   }
   __syncthreads();
 }
 
-// A walk over the units of one cluster: u, u + step, ... The expert only moves
-// forward.
-template <int BN>
+// A walk over the units u, u + step, ... of one cluster. The expert only
+// moves forward.
+template <int BN, bool GROUPED>
 struct Walk {
   int u, step, total, e = 0;
   int tile, row, ntok;  // of the current unit: tile of W, first row, rows
   __device__ __forceinline__ Walk(const Ranges& R, const MmArgs& a, int first, int stride)
-      : u(first), step(stride), total(R.unit0[a.n_experts] * a.n_tiles) {}
+      : u(first), step(stride), total((GROUPED ? R.unit0[a.n_experts] : (a.M + BN - 1) / BN) * a.n_tiles) {}
   __device__ __forceinline__ bool get(const Ranges& R, const MmArgs& a) {
     if (u >= total) return false;
-    while (R.unit0[e + 1] * a.n_tiles <= u) ++e;
-    const int n_tb = R.unit0[e + 1] - R.unit0[e];
-    const int local = u - R.unit0[e] * a.n_tiles;
+    int n_tb = (a.M + BN - 1) / BN, local = u, first = 0, rows = a.M;
+    if (GROUPED) {
+      while (R.unit0[e + 1] * a.n_tiles <= u) ++e;
+      n_tb = R.unit0[e + 1] - R.unit0[e];
+      local = u - R.unit0[e] * a.n_tiles;
+      first = R.first[e];
+      rows = R.rows[e];
+    }
     tile = local / n_tb;
     const int tb = local - tile * n_tb;
-    row = R.first[e] + tb * BN;
-    ntok = min(BN, R.rows[e] - tb * BN);
+    row = first + tb * BN;
+    ntok = min(BN, rows - tb * BN);
     return true;
   }
   __device__ __forceinline__ void next() { u += step; }
@@ -178,28 +215,33 @@ struct Walk {
 constexpr int kSkThreads = 256;
 template <int BN>
 struct Sk {
+  static constexpr int kPer = BN <= 64 ? 2 : 1;  // blocks of K per stage
   static constexpr int kXBytes = BN * kFp8Block;
-  static constexpr int kStage = kFp8TileBytes + kXBytes;
-  static constexpr int kSlots = BN <= 16 ? 9 : BN <= 32 ? 8 : BN <= 64 ? 7 : 4;  // TMA ring
-  static constexpr int kAcc = BN <= 64 ? 4 : 4;                                  // P_b ring in TMEM
-  static constexpr int kCols = kAcc * BN < 32 ? 32 : kAcc * BN;                  // a power of two
-  static constexpr int kRecv = BN * kFp8Block * 4;                               // cluster sums
+  static constexpr int kStage = kPer * (kFp8TileBytes + kXBytes);
+  static constexpr int kSlots = BN <= 16 ? 5 : BN <= 32 ? 4 : BN <= 64 ? 3 : 4;  // operands in, P out (TMEM)
+  static constexpr int kUsed = kSlots * kPer * BN;
+  static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;    // allocated: a power of two
+  static constexpr int kSc = 8;                                                  // ring of activation scales
+  static constexpr int kMaxCluster = 16;
+  static constexpr int kRecv = (BN + kMaxCluster) * kFp8Block * 4;               // cluster sums
   static constexpr size_t smem(int E) { return 1024 + (size_t)kSlots * kStage + kRecv + ranges_bytes(E); }
 };
 
-template <int BN>
+template <int BN, bool GROUPED>
 __global__ void __launch_bounds__(kSkThreads, 1)
 fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx, MmArgs a,
-                  int cluster) {
+                  int cluster, int own, int own_inv) {
   using C = Sk<BN>;
-  constexpr int S = C::kSlots, A = C::kAcc;
+  constexpr int S = C::kSlots, KP = C::kPer, SC = C::kSc;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
   float* recv = reinterpret_cast<float*>(ring + S * C::kStage);  // [source rank][own column][128 rows]
   const Ranges R = ranges_at(reinterpret_cast<uint8_t*>(recv) + C::kRecv, a.n_experts);
-  __shared__ uint64_t bar_full[S], bar_empty[S], bar_p[A], bar_pfree[A], bar_s[A], bar_drain;
+  // stage i: operands landed (full), their products are in TMEM (p: the
+  // operands' slot is free too), the products have been read (pfree)
+  __shared__ uint64_t bar_full[S], bar_p[S], bar_pfree[S], bar_s[SC], bar_sfree[SC], bar_drain;
   __shared__ uint64_t bar_recv[4], bar_rfree[4];  // per quadrant of rows
-  __shared__ __align__(16) float sc[A][BN + 4];   // the block's activation scales, then the tile's scale
+  __shared__ __align__(16) float sc[SC][KP][BN + 4];  // a block's activation scales, then the tile's scale
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
 
@@ -210,211 +252,344 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
   volatile int* abrt = &abort_sh;
 
   pdl_launch_dependents();
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&bar_full[i], 1);
-      mbar_init(&bar_empty[i], 1);
+  // a stage's weights and activations into its slot
+  auto load_w = [&](int tile0, int kb, int slot) {
+    uint8_t* p = ring + slot * C::kStage;
+    const int nk = min(KP, kb1 - kb);
+    mbar_arrive_expect_tx(&bar_full[slot], nk * (kFp8TileBytes + C::kXBytes));
+    for (int j = 0; j < nk; ++j)
+      tma_load_2d(p + j * kFp8TileBytes, &tmw, &bar_full[slot], 0, (tile0 + kb + j) * kFp8Block);
+  };
+  auto load_x = [&](int row, int kb, int slot) {
+    uint8_t* p = ring + slot * C::kStage + KP * kFp8TileBytes;
+    for (int j = 0; j < min(KP, kb1 - kb); ++j)
+      tma_load_2d(p + j * C::kXBytes, &tmx, &bar_full[slot], (kb + j) * kFp8Block, row);
+  };
+  // One layer: the first stages' weights are on their way before the rest is
+  // set up, and before the previous kernel has finished.
+  const int ahead = !GROUPED && my < a.n_tiles * ((a.M + BN - 1) / BN) ? min(S, (kb1 - kb0 + KP - 1) / KP) : 0;
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int i = 0; i < S; ++i) mbar_init(&bar_full[i], 1);
+      fence_mbar_init();
+      prefetch_tmap(&tmx);
+      const int tile = my / ((a.M + BN - 1) / BN);
+      for (int i = 0; i < ahead; ++i) load_w(tile * a.n_blocks, kb0 + i * KP, i);
     }
-    for (int i = 0; i < A; ++i) {
-      mbar_init(&bar_p[i], 1);
-      mbar_init(&bar_pfree[i], 4);
-      mbar_init(&bar_s[i], 32);
+  } else if (warp == 1) {
+    if (elect_one()) {
+      for (int i = 0; i < S; ++i) {
+        mbar_init(&bar_p[i], 1);
+        mbar_init(&bar_pfree[i], 4);
+      }
+      for (int i = 0; i < SC; ++i) {
+        mbar_init(&bar_s[i], 32);
+        mbar_init(&bar_sfree[i], 4);
+      }
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&bar_recv[i], cluster);
+        mbar_init(&bar_rfree[i], cluster);
+      }
+      mbar_init(&bar_drain, 1);
+      abort_sh = 0;
+      fence_mbar_init();
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(&bar_recv[i], cluster);
-      mbar_init(&bar_rfree[i], cluster);
-    }
-    mbar_init(&bar_drain, 1);
-    abort_sh = 0;
-    fence_mbar_init();
-  }
-  if (warp == 0 && lane == 0) {
-    prefetch_tmap(&tmw);
-    prefetch_tmap(&tmx);
-  }
-  if (warp == 2) {
+  } else if (warp == 2) {
     tmem_alloc(&tmem_sh, C::kCols);
     tmem_relinquish();
   }
-  // everything the previous kernel may have written (x, scales, offsets) or
-  // still read (y) is touched after this
-  pdl_wait();
+  __syncwarp();
+  // what the previous kernel may have written (x, scales, offsets) or still
+  // read (y) is touched after pdl_wait
+  if (GROUPED) pdl_wait();
   tc_fence_before();
-  load_ranges<BN>(R, a);  // (has the CTA's barriers)
+  load_ranges<BN, GROUPED>(R, a);  // (has the CTA's barrier)
   tc_fence_after();
   if (cluster > 1) {  // the others' barriers exist before they are arrived on
-    cluster_arrive_release();
+    cluster_arrive_relaxed();
     cluster_wait();
   }
   const uint32_t tmem = tmem_sh;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int issued = 0, b = 0;
-      uint32_t ph = 0;
-      bool ok = true;
-      for (Walk<BN> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
-        const int t0 = (w.e * a.n_tiles + w.tile) * a.n_blocks;
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!(ok = mbar_wait(&bar_empty[b], ph ^ 1, abrt, 32))) break;
-          uint8_t* slot = ring + b * C::kStage;
-          mbar_arrive_expect_tx(&bar_full[b], C::kStage);
-          tma_load_2d(slot, &tmw, &bar_full[b], 0, (t0 + kb) * kFp8Block);
-          tma_load_2d(slot + kFp8TileBytes, &tmx, &bar_full[b], kb * kFp8Block, w.row);
-          ++issued;
-          if (++b == S) b = 0, ph ^= 1;
-        }
+    int issued = ahead, b = ahead;
+    uint32_t ph = 0;
+    if (b == S) b = 0, ph ^= 1;
+    bool ok = true, first = true;
+    pdl_wait();
+    for (Walk<BN, GROUPED> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
+      const int t0 = (w.e * a.n_tiles + w.tile) * a.n_blocks;
+      int kb = kb0;
+      if (first) {
+        first = false;
+        if (elect_one())
+          for (int i = 0; i < ahead; ++i) load_x(w.row, kb0 + i * KP, i);
+        __syncwarp();
+        kb += ahead * KP;
       }
-      if (*abrt) {  // let the copies this thread issued land before the CTA ends
-        volatile int never = 0;
-        for (int i = max(0, issued - S); i < issued; ++i) mbar_wait(&bar_full[i % S], (i / S) & 1, &never);
+      for (; kb < kb1; kb += KP) {
+        if (!(ok = wait_bar_warp(&bar_p[b], ph ^ 1, abrt))) break;
+        if (elect_one()) {
+          load_w(t0, kb, b);
+          load_x(w.row, kb, b);
+        }
+        __syncwarp();
+        ++issued;
+        if (++b == S) b = 0, ph ^= 1;
       }
     }
+    if (*abrt) {  // let the copies this warp issued land before the CTA ends
+      volatile int never = 0;
+      for (int i = max(0, issued - S); i < issued; ++i) wait_bar(&bar_full[i % S], (i / S) & 1, &never);
+    }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int b = 0, p = 0;
-      uint32_t ph = 0, pph = 0;
-      bool ok = true;
-      for (Walk<BN> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
-        const uint32_t idesc = idesc_e4m3(128, (w.ntok + 15) / 16 * 16);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!(ok = mbar_wait(&bar_pfree[p], pph ^ 1, abrt) && mbar_wait(&bar_full[b], ph, abrt))) break;
-          tc_fence_after();
-          const uint32_t wa = smem_u32(ring + b * C::kStage);
+    int b = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (Walk<BN, GROUPED> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
+      const uint32_t idesc = idesc_e4m3(128, (w.ntok + 15) / 16 * 16);
+      for (int kb = kb0; kb < kb1; kb += KP) {
+        // (odd lanes wait for the operands, even lanes for the TMEM slot)
+        if (!(ok = wait_bar_warp(lane & 1 ? &bar_full[b] : &bar_pfree[b], lane & 1 ? ph : ph ^ 1, abrt))) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t wd = smem_desc(smem_u32(ring + b * C::kStage));
+          const uint64_t xd = smem_desc(smem_u32(ring + b * C::kStage + KP * kFp8TileBytes));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_f8(tmem + p * BN, smem_desc(wa + kk * 32), smem_desc(wa + kFp8TileBytes + kk * 32), idesc, kk > 0);
-          tc_commit(&bar_empty[b]);
-          tc_commit(&bar_p[p]);
-          if (++b == S) b = 0, ph ^= 1;
-          if (++p == A) p = 0, pph ^= 1;
+          for (int j = 0; j < KP; ++j) {
+            if (kb + j < kb1) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)  // 32 columns of K each: 2 units of 16 bytes
+                tc_mma_f8(tmem + (b * KP + j) * BN, wd + (j * kFp8TileBytes >> 4) + kk * 2,
+                          xd + (j * C::kXBytes >> 4) + kk * 2, idesc, kk > 0);
+            }
+          }
+          tc_commit(&bar_p[b]);
         }
+        __syncwarp();
+        if (++b == S) b = 0, ph ^= 1;
       }
-      if (*abrt) {  // let issued MMAs finish before TMEM is freed
-        volatile int never = 0;
-        tc_commit(&bar_drain);
-        mbar_wait(&bar_drain, 0, &never);
-      }
+    }
+    if (*abrt) {  // let issued MMAs finish before TMEM is freed
+      volatile int never = 0;
+      if (elect_one()) tc_commit(&bar_drain);
+      __syncwarp();
+      wait_bar(&bar_drain, 0, &never);
     }
   } else if (warp == 3) {
     int p = 0;
-    uint32_t pph = 0;
+    uint32_t ph = 0;
     bool ok = true;
-    for (Walk<BN> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
+    pdl_wait();
+    for (Walk<BN, GROUPED> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
       const float* ws = a.ws + (size_t)(w.e * a.n_tiles + w.tile) * a.n_blocks;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = mbar_wait(&bar_pfree[p], pph ^ 1, abrt, 32))) break;
+      const float* xs = a.xs + (size_t)w.row * a.n_blocks;
+      for (int kb = kb0; kb < kb1; kb += KP) {
+        if (!(ok = wait_bar_warp(&bar_sfree[p], ph ^ 1, abrt))) break;
 #pragma unroll
-        for (int c = lane; c < BN; c += 32)  // columns past the tokens take the last one's scale
-          cp_async4(&sc[p][c], a.xs + (size_t)(w.row + min(c, w.ntok - 1)) * a.n_blocks + kb);
-        if (lane == 0) cp_async4(&sc[p][BN], ws + kb);
+        for (int i = lane; i < BN * KP; i += 32) {  // (columns past the tokens are never used)
+          const int c = i / KP, j = i % KP;
+          if (c < w.ntok && kb + j < kb1) cp_async4(&sc[p][j][c], xs + (size_t)c * a.n_blocks + kb + j);
+        }
+        if (lane < KP && kb + lane < kb1) cp_async4(&sc[p][lane][BN], ws + kb + lane);
         cp_async_arrive(&bar_s[p]);
-        if (++p == A) p = 0, pph ^= 1;
+        if (++p == SC) p = 0, ph ^= 1;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= 4) {
     const int q = warp & 3, r = q * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
-    const int cpr = BN / cluster;  // columns each rank adds up
-    int p = 0;
-    uint32_t pph = 0, uph = 0;
+    int p = 0, sp = 0;
+    uint32_t pph = 0, sph = 0, uph = 0;
     bool ok = true;
-    for (Walk<BN> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
+    pdl_wait();  // y
+    constexpr int CW = BN < 32 ? BN : 32;  // columns per load
+    constexpr int NC = BN / CW;
+    for (Walk<BN, GROUPED> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
+      const int n_out = w.tile * kFp8Block + r;
+      const float bias = a.out.bias && n_out < a.N ? __ldg(a.out.bias + (size_t)w.e * a.N + n_out) : 0.f;
       float acc[BN];
 #pragma unroll
       for (int c = 0; c < BN; ++c) acc[c] = 0.f;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!(ok = mbar_wait(&bar_s[p], pph, abrt) && mbar_wait(&bar_p[p], pph, abrt))) break;
+      for (int kb = kb0; kb < kb1; kb += KP) {
+        const int nk = min(KP, kb1 - kb);
+        if (!(ok = wait_bar_warp(lane & 1 ? &bar_p[p] : &bar_s[sp], lane & 1 ? pph : sph, abrt))) break;
         tc_fence_after();
-        const float wsc = sc[p][BN];
+        // P in pieces of CW columns, the next piece loading while this one is added
+        uint32_t d[2][CW];
+        auto live = [&](int i) { return i / NC < nk && i % NC * CW < w.ntok; };
+        auto load = [&](int i) {
+          const uint32_t at = lane_base + (p * KP + i / NC) * BN + i % NC * CW;
+          tmem_ld16(at, *reinterpret_cast<uint32_t(*)[16]>(d[i & 1]));
+          if (CW > 16) tmem_ld16(at + 16, *reinterpret_cast<uint32_t(*)[16]>(d[i & 1] + CW - 16));
+        };
+        load(0);
 #pragma unroll
-        for (int c0 = 0; c0 < BN; c0 += 16) {
-          if (c0 < w.ntok) {
-            uint32_t d[16];
-            tmem_ld16(lane_base + p * BN + c0, d);
-            tmem_wait_ld();
+        for (int i = 0; i < KP * NC; ++i) {
+          if (live(i)) tmem_wait_ld();
+          if (i + 1 < KP * NC && live(i + 1)) load(i + 1);
+          if (!live(i)) continue;
+          const float* s = sc[sp][i / NC];
+          const float ws = s[BN];
+          const int c0 = i % NC * CW;
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) {
-              const float4 s4 = *reinterpret_cast<const float4*>(&sc[p][c0 + j]);
-              acc[c0 + j] = fmaf(__uint_as_float(d[j]) * s4.x, wsc, acc[c0 + j]);
-              acc[c0 + j + 1] = fmaf(__uint_as_float(d[j + 1]) * s4.y, wsc, acc[c0 + j + 1]);
-              acc[c0 + j + 2] = fmaf(__uint_as_float(d[j + 2]) * s4.z, wsc, acc[c0 + j + 2]);
-              acc[c0 + j + 3] = fmaf(__uint_as_float(d[j + 3]) * s4.w, wsc, acc[c0 + j + 3]);
-            }
+          for (int j = 0; j < CW; j += 4) {
+            const float4 s4 = *reinterpret_cast<const float4*>(s + c0 + j);
+            const uint32_t(&v)[CW] = d[i & 1];
+            acc[c0 + j] = fmaf(__uint_as_float(v[j]) * s4.x, ws, acc[c0 + j]);
+            acc[c0 + j + 1] = fmaf(__uint_as_float(v[j + 1]) * s4.y, ws, acc[c0 + j + 1]);
+            acc[c0 + j + 2] = fmaf(__uint_as_float(v[j + 2]) * s4.z, ws, acc[c0 + j + 2]);
+            acc[c0 + j + 3] = fmaf(__uint_as_float(v[j + 3]) * s4.w, ws, acc[c0 + j + 3]);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_pfree[p]);
-        if (++p == A) p = 0, pph ^= 1;
+        if (lane == 0) {
+          mbar_arrive(&bar_pfree[p]);
+          mbar_arrive(&bar_sfree[sp]);
+        }
+        if (++p == S) p = 0, pph ^= 1;
+        if (++sp == SC) sp = 0, sph ^= 1;
       }
       if (!ok) break;
-      const int n = w.tile * kFp8Block + r;
-      Out o{a.out.y, a.out.bias ? a.out.bias + (size_t)w.e * a.N : nullptr, a.out.bf16};
       if (cluster == 1) {
-        if (n < a.N) {
+        if (n_out < a.N) {
 #pragma unroll
           for (int c = 0; c < BN; ++c)
-            if (c < w.ntok) store_out(o, (size_t)(w.row + c) * a.N + n, n, acc[c]);
+            if (c < w.ntok) put_out(a.out, (size_t)(w.row + c) * a.N + n_out, acc[c] + bias);
         }
         continue;
       }
-      // this rank's sums of column c to slot [rank][c % cpr] of the rank that owns c
-      if (!(ok = mbar_wait_cluster(&bar_rfree[q], uph ^ 1, abrt))) break;
-      const uint32_t mine = smem_u32(recv) + (uint32_t)(rank * cpr * kFp8Block + r) * 4u;
+      // this rank's sums of column c to slot [rank][c % own] of the rank c / own that adds column c
+      if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(&bar_rfree[q], uph ^ 1, abrt)))) break;
+      const uint32_t mine = smem_u32(recv) + (uint32_t)(rank * own * kFp8Block + r) * 4u;
 #pragma unroll
       for (int c = 0; c < BN; ++c)
         if (c < w.ntok) {
-          const int dst = c / cpr;
-          st_cluster_f32(map_to_rank(mine + (uint32_t)((c - dst * cpr) * kFp8Block) * 4u, dst), acc[c]);
+          const int dst = (c * own_inv) >> 16;
+          st_cluster_f32(map_to_rank(mine + (uint32_t)((c - dst * own) * kFp8Block) * 4u, dst), acc[c]);
         }
       __syncwarp();
       if (lane < cluster) mbar_arrive_rank(&bar_recv[q], lane);
-      if (!(ok = mbar_wait_cluster(&bar_recv[q], uph, abrt))) break;
-      for (int c = 0; c < cpr; ++c) {
-        const int col = rank * cpr + c;
-        if (col >= w.ntok) break;
+      if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(&bar_recv[q], uph, abrt)))) break;
+      const int mine_n = min(own, w.ntok - rank * own);
+#pragma unroll 4
+      for (int c = 0; c < mine_n; ++c) {
         float v = 0.f;
-        for (int s = 0; s < cluster; ++s) v += recv[(s * cpr + c) * kFp8Block + r];
-        if (n < a.N) store_out(o, (size_t)(w.row + col) * a.N + n, n, v);
+#pragma unroll 4
+        for (int s = 0; s < cluster; ++s) v += recv[(s * own + c) * kFp8Block + r];
+        if (n_out < a.N) put_out(a.out, (size_t)(w.row + rank * own + c) * a.N + n_out, v + bias);
       }
-      __syncwarp();
-      if (lane < cluster) mbar_arrive_rank(&bar_rfree[q], lane);
+      if (w.u + w.step < w.total) {  // nobody waits for the last unit's
+        __syncwarp();
+        if (lane < cluster) mbar_arrive_rank(&bar_rfree[q], lane);
+      }
       uph ^= 1;
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  if (cluster > 1) cluster_arrive_relaxed();
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
   if (*abrt && threadIdx.x == 0) atomicOr(a.status, kStatusWaitTimeout);
-  if (cluster > 1) {  // no CTA leaves while another may still store into its shared memory
-    cluster_arrive_release();
+  if (cluster > 1) {  // no CTA leaves while another may still reach into its shared memory
+    __syncwarp();
     cluster_wait();
   }
 }
 
-template <int BN>
+// Clusters of c CTAs of `kern` that fit on the GPU at once, for c = 1 .. 16
+// (0: none). Asked once per (device, kernel).
+struct ClusterFit {
+  const void* kern;
+  int device;
+  int fit[17];
+};
+cudaError_t cluster_fit(const void* kern, int device, size_t smem, const int** fit) {
+  static std::mutex mu;
+  static std::vector<std::unique_ptr<ClusterFit>> known;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const auto& k : known)
+    if (k->kern == kern && k->device == device) {
+      *fit = k->fit;
+      return cudaSuccess;
+    }
+  cudaError_t e = allow_max_smem(kern);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  std::unique_ptr<ClusterFit> f(new (std::nothrow) ClusterFit{kern, device, {}});
+  if (!f) return cudaErrorMemoryAllocation;
+  for (int c = 1; c <= 16; ++c) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kSkThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&f->fit[c], kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      f->fit[c] = 0;
+    }
+  }
+  try {
+    known.push_back(std::move(f));
+  } catch (const std::bad_alloc&) {
+    return cudaErrorMemoryAllocation;
+  }
+  *fit = known.back()->fit;
+  return cudaSuccess;
+}
+
+template <int BN, bool GROUPED>
 cudaError_t launch_skinny(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cudaStream_t s) {
   CUtensorMap tmx;
   cudaError_t e = fp8_tensor_map(&tmx, xq, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)fp8_ld(a.K), BN);
   if (e != cudaSuccess) return e;
-  auto kern = fp8_skinny_kernel<BN>;
-  if ((e = allow_max_smem(reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
-  // units: exact for one layer; for experts every expert with rows has at
-  // least one token block and at most one that is not full
-  const int64_t most = (int64_t)a.n_tiles * (std::min(a.n_experts, a.M) + (a.n_experts > 1 ? a.M / BN : (a.M - 1) / BN));
-  // as many CTAs on a unit as leave the GPU's SMs one each, and every CTA two blocks of K
+  auto kern = fp8_skinny_kernel<BN, GROUPED>;
+  const size_t smem = Sk<BN>::smem(GROUPED ? a.n_experts : 0);
+  const int* fit = nullptr;
+  if ((e = cluster_fit(reinterpret_cast<const void*>(kern), h.device, Sk<BN>::smem(GROUPED ? kFp8MaxExperts : 0), &fit)) !=
+      cudaSuccess)
+    return e;
+  // units: exact for one layer; experts with rows have at most one block of
+  // tokens that is not full, and about min(experts, rows) have rows
+  const int used = std::min(a.n_experts, a.M);
+  const int64_t most = (int64_t)a.n_tiles * (GROUPED ? used + a.M / BN : (a.M + BN - 1) / BN);
+  const int64_t likely = (int64_t)a.n_tiles * std::max<int64_t>(GROUPED ? used : 0, (a.M + BN - 1) / BN);
+  // CTAs per unit: the blocks of K that the busiest cluster's CTAs work
+  // through one after another, plus what a unit's exchange costs
   int c = 1;
-  while (c < 8 && most * c * 2 <= h.num_sms && c * 4 <= a.n_blocks) c *= 2;
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(most, h.num_sms / c)) * c;
-  if (c == 1) return launch_pdl(kern, (unsigned)grid, kSkThreads, Sk<BN>::smem(a.n_experts), s, h.tm_w, tmx, a, c);
-  return launch_pdl_cluster(kern, (unsigned)grid, kSkThreads, Sk<BN>::smem(a.n_experts), (unsigned)c, s, h.tm_w, tmx,
-                            a, c);
+  int64_t best = INT64_MAX;
+  for (int t = 1; t <= Sk<BN>::kMaxCluster && t <= a.n_blocks; ++t) {
+    if (fit[t] < 1) continue;
+    const int64_t rounds = (likely + fit[t] - 1) / fit[t];
+    const int64_t cost = rounds * ((a.n_blocks + t - 1) / t + (t > 1 ? 2 : 0)) + (t > 1 ? 6 : 0);
+    if (cost < best) best = cost, c = t;
+  }
+  const int own = (BN + c - 1) / c;
+  const int own_inv = (65536 + own - 1) / own;  // (c * own_inv) >> 16 = c / own for c < BN
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(most, fit[c])) * c;
+  if (c == 1) return launch_pdl(kern, (unsigned)grid, kSkThreads, smem, s, h.tm_w, tmx, a, c, own, own_inv);
+  return launch_pdl_cluster(kern, (unsigned)grid, kSkThreads, smem, (unsigned)c, s, h.tm_w, tmx, a, c, own, own_inv);
+}
+
+template <bool GROUPED>
+cudaError_t launch_mm(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cudaStream_t s) {
+  // tokens an expert gets on average decide the block of tokens
+  const int per = GROUPED ? (a.M + a.n_experts - 1) / a.n_experts : a.M;
+  if (per <= 16) return launch_skinny<16, GROUPED>(h, xq, a, s);
+  if (per <= 32) return launch_skinny<32, GROUPED>(h, xq, a, s);
+  if (per <= 64) return launch_skinny<64, GROUPED>(h, xq, a, s);
+  return launch_skinny<128, GROUPED>(h, xq, a, s);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -449,12 +624,7 @@ cudaError_t fp8_tensor_map(CUtensorMap* tm, const void* base, uint64_t cols, uin
 cudaError_t launch_fp8_mm(const hxq_fp8& h, const uint8_t* xq, const float* xs, const int* offsets, const Fp8Out& out,
                           int M, cudaStream_t s) {
   const MmArgs a{xs, h.d_ws, offsets, out, M, h.N, h.K, h.n_tiles, h.n_blocks, h.n_experts, h.d_status};
-  // tokens an expert gets on average decide the block of tokens
-  const int per = (M + h.n_experts - 1) / h.n_experts;
-  if (per <= 16) return launch_skinny<16>(h, xq, a, s);
-  if (per <= 32) return launch_skinny<32>(h, xq, a, s);
-  if (per <= 64) return launch_skinny<64>(h, xq, a, s);
-  return launch_skinny<128>(h, xq, a, s);
+  return offsets ? launch_mm<true>(h, xq, a, s) : launch_mm<false>(h, xq, a, s);
 }
 
 }  // namespace hxq
