@@ -35,7 +35,8 @@ struct hxq_fp8 {
   uint8_t* d_w;
   float* d_ws;
   int* d_status;     // device-side error word (bounded waits that gave up)
-  CUtensorMap tm_w;  // the tiles as rows of 128 bytes, box 128 x 128, 128-byte swizzle
+  // the tiles as rows of 128 bytes in the 128-byte swizzle, boxes of 128, 64 and 32 rows
+  CUtensorMap tm_w, tm_w64, tm_w32;
 };
 
 namespace hxq {

@@ -137,9 +137,14 @@ int hxq_fp8_create(const uint8_t* W, const float* scales, int n_experts, int N, 
     cudaGetLastError();
     return HXQ_EUNSUPPORTED;
   }
-  cudaDeviceProp prop;
-  if (cudaGetDeviceProperties(&prop, dev) != cudaSuccess) return HXQ_ECUDA;
-  if (prop.major != 10 || prop.minor != 0) return HXQ_EUNSUPPORTED;
+  int major = 0, minor = 0, sms = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return HXQ_ECUDA;
+  }
+  if (major != 10 || minor != 0) return HXQ_EUNSUPPORTED;
 
   hxq_fp8* h = new (std::nothrow) hxq_fp8();
   if (!h) return HXQ_ENOMEM;
@@ -149,7 +154,7 @@ int hxq_fp8_create(const uint8_t* W, const float* scales, int n_experts, int N, 
   h->n_tiles = nt;
   h->n_blocks = kb;
   h->device = dev;
-  h->num_sms = prop.multiProcessorCount;
+  h->num_sms = sms;
   const size_t tiles = (size_t)n_experts * nt * kb, per = (size_t)nt * kb * hxq::kFp8TileBytes;
   const size_t src = (size_t)N * K;
   uint8_t* d_src = nullptr;  // one expert's weights as given
@@ -167,8 +172,9 @@ int hxq_fp8_create(const uint8_t* W, const float* scales, int n_experts, int N, 
   }
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   cudaFree(d_src);
-  if (e == cudaSuccess)
-    e = hxq::fp8_tensor_map(&h->tm_w, h->d_w, hxq::kFp8Block, tiles * hxq::kFp8Block, hxq::kFp8Block, hxq::kFp8Block);
+  CUtensorMap* const maps[] = {&h->tm_w, &h->tm_w64, &h->tm_w32};
+  for (int i = 0; e == cudaSuccess && i < 3; ++i)
+    e = hxq::fp8_tensor_map(maps[i], h->d_w, hxq::kFp8Block, tiles * hxq::kFp8Block, hxq::kFp8Block, 128u >> i);
   if (e != cudaSuccess) {
     free_fp8(h);
     cudaGetLastError();

@@ -582,6 +582,409 @@ cudaError_t launch_skinny(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, 
   return launch_pdl_cluster(kern, (unsigned)grid, kSkThreads, smem, (unsigned)c, s, h.tm_w, tmx, a, c, own, own_inv);
 }
 
+// ---- many tokens ----------------------------------------------------------------
+//
+// fp8_wide_kernel: D = x . W^T, lanes = tokens, columns = features, by pairs
+// of CTAs (tcgen05 cta_group::2): 256 tokens x 256 features a pair, each CTA
+// holding 128 of the tokens and 128 of the features' rows in shared memory
+// and its 128 tokens x 256 features of D in TMEM, twice. With tokens on the
+// lanes a thread needs one scale per block of K (its token's times its
+// tile's), so adding P_b is one multiply-add per element.
+//
+// The units are (expert, 256 tokens, two tiles of W), token blocks fastest,
+// one after another on each pair; what does not fill the last round of all
+// pairs is cut into pieces of 128 or 64 features.
+
+constexpr int kWideTokens = 256;
+constexpr int kWideSlots = 6;
+constexpr int kWideStage = 2 * kFp8TileBytes;  // 128 tokens and up to 128 features of one block of K
+constexpr int kWideThreads = 384;              // 4 warps of control, 8 that add and store
+constexpr int kWideCtlRegs = 40, kWideEpiRegs = 224;  // 128 * 40 + 256 * 224 <= 384 * 168
+constexpr size_t wide_smem(int E) { return 1024 + (size_t)kWideSlots * kWideStage + ranges_bytes(E); }
+
+struct WideWalk {
+  int item, step, items, full, cut, cu_n, e = 0;
+  int cu, row, ntok;     // of the current unit: pair of tiles, first row, rows
+  int width, piece;      // features of the piece, and which
+  __device__ __forceinline__ WideWalk(const Ranges& R, const MmArgs& a, bool grouped, int first, int pairs)
+      : item(first), step(pairs), cu_n((a.n_tiles + 1) / 2) {
+    const int units = (grouped ? R.unit0[a.n_experts] : (a.M + kWideTokens - 1) / kWideTokens) * cu_n;
+    full = units / pairs * pairs;
+    const int rest = units - full;
+    cut = rest * 4 <= pairs ? 4 : rest * 2 <= pairs ? 2 : 1;
+    items = full + rest * cut;
+  }
+  // The next item with work, or false.
+  __device__ __forceinline__ bool get(const Ranges& R, const MmArgs& a, bool grouped) {
+    for (;; item += step) {
+      if (item >= items) return false;
+      int u = item;
+      width = 256;
+      piece = 0;
+      if (u >= full) {
+        u = full + (item - full) / cut;
+        piece = (item - full) % cut;
+        width = 256 / cut;
+      }
+      int n_tb = (a.M + kWideTokens - 1) / kWideTokens, local = u, first = 0, rows = a.M;
+      if (grouped) {
+        while (R.unit0[e + 1] * cu_n <= u) ++e;
+        n_tb = R.unit0[e + 1] - R.unit0[e];
+        local = u - R.unit0[e] * cu_n;
+        first = R.first[e];
+        rows = R.rows[e];
+      }
+      cu = local / n_tb;
+      const int tb = local - cu * n_tb;
+      row = first + tb * kWideTokens;
+      ntok = min(kWideTokens, rows - tb * kWideTokens);
+      const int have = 2 * cu + 1 < a.n_tiles ? 256 : 128;  // an odd last tile stands alone
+      width = min(width, have);
+      if (piece * width < have) return true;
+    }
+  }
+  // Tile of W of the features from piece * width + off on.
+  __device__ __forceinline__ int tile(int off) const { return 2 * cu + (piece * width + off) / kFp8Block; }
+};
+
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+               ::"r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tc_mma2_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this address in both CTAs of the pair.
+__device__ __forceinline__ void tc_commit2(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+      ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+      : "memory");
+}
+// This CTA's shared memory <- global; the bytes are counted on the barrier `bar` (an address from map_to_rank) of
+// either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+      "%3}], [%4];"
+      ::"r"(smem_u32(dst)), "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(v));
+  tmem_ld16(taddr + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+}
+// (a0, a1) += (d0, d1) * (s, s)
+__device__ __forceinline__ void fma2(float2& a, uint32_t d0, uint32_t d1, float s) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%0, %1};\n\t"
+      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "+f"(a.x), "+f"(a.y)
+      : "r"(d0), "r"(d1), "f"(s));
+}
+
+// 32 consecutive outputs of one row; n of them exist. vec: bytes a store may
+// take (32, 16, or 0 for single elements).
+__device__ __forceinline__ void store_row32(const Fp8Out& o, size_t at, int n, int vec, const float (&v)[32]) {
+  if (o.bf16) {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o.y) + at;
+    if (vec && n >= 32) {
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      if (vec == 32) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 8)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                       ::"l"(p + 2 * j), "r"(w[j]), "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]),
+                         "r"(w[j + 5]), "r"(w[j + 6]), "r"(w[j + 7])
+                       : "memory");
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; j += 4)
+          *reinterpret_cast<uint4*>(p + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) p[j] = __float2bfloat16_rn(v[j]);
+    }
+  } else {
+    float* p = static_cast<float*>(o.y) + at;
+    if (vec && n >= 32) {
+      if (vec == 32) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                       ::"l"(p + j), "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]),
+                         "f"(v[j + 5]), "f"(v[j + 6]), "f"(v[j + 7])
+                       : "memory");
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) p[j] = v[j];
+    }
+  }
+}
+
+struct WideMaps {
+  CUtensorMap x;      // 128 tokens
+  CUtensorMap w[3];   // 128, 64, 32 rows of a tile
+};
+
+template <bool GROUPED>
+__global__ void __launch_bounds__(kWideThreads, 1)
+fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int vec) {
+  constexpr int S = kWideSlots;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
+  const Ranges R = ranges_at(ring + S * kWideStage, a.n_experts);
+  // full and pfree are used in the leading CTA only; empty and p arrive in both
+  __shared__ uint64_t bar_full[S], bar_empty[S], bar_p[2], bar_pfree[2], bar_drain;
+  __shared__ uint32_t tmem_sh;
+  __shared__ int abort_sh;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  volatile int* abrt = &abort_sh;
+
+  pdl_launch_dependents();
+  if (warp == 0 && elect_one()) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&bar_full[i], 1);
+      mbar_init(&bar_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_p[i], 1);
+      mbar_init(&bar_pfree[i], 16);
+    }
+    mbar_init(&bar_drain, 1);
+    abort_sh = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.x);
+    prefetch_tmap(&maps.w[0]);
+  }
+  __syncwarp();
+  if (warp == 2) {
+    tmem_alloc2(&tmem_sh, 512);
+    tmem_relinquish2();
+  }
+  if (GROUPED) pdl_wait();
+  tc_fence_before();
+  load_ranges<kWideTokens, GROUPED>(R, a);
+  tc_fence_after();
+  cluster_arrive_relaxed();
+  cluster_wait();
+  const uint32_t tmem = tmem_sh;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWideCtlRegs));
+    if (warp == 0) {
+      int issued = 0, b = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      pdl_wait();
+      for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
+        // this CTA's rows of W: a tile of its own, or its half of the piece
+        const int rows = w.width / 2;
+        const CUtensorMap* tw = rows == 128 ? &maps.w[0] : rows == 64 ? &maps.w[1] : &maps.w[2];
+        const int off = rank * rows;
+        const int w0 = (w.e * a.n_tiles + w.tile(off)) * a.n_blocks * kFp8Block + (w.piece * w.width + off) % kFp8Block;
+        const int x0 = w.row + rank * 128;
+        for (int kb = 0; kb < a.n_blocks; ++kb) {
+          if (!(ok = wait_bar_warp(&bar_empty[b], ph ^ 1, abrt))) break;
+          if (elect_one()) {
+            if (rank == 0) mbar_arrive_expect_tx(&bar_full[b], 2 * (kFp8TileBytes + rows * kFp8Block));
+            const uint32_t bar = map_to_rank(smem_u32(&bar_full[b]), 0);
+            uint8_t* slot = ring + b * kWideStage;
+            tma_load_2d_pair(slot, &maps.x, bar, kb * kFp8Block, x0);
+            tma_load_2d_pair(slot + kFp8TileBytes, tw, bar, 0, w0 + kb * kFp8Block);
+          }
+          __syncwarp();
+          ++issued;
+          if (++b == S) b = 0, ph ^= 1;
+        }
+      }
+      if (*abrt && rank == 0) {  // let the copies land before the CTA ends (the other CTA's are counted here too)
+        volatile int never = 0;
+        for (int i = max(0, issued - S); i < issued; ++i) wait_bar(&bar_full[i % S], (i / S) & 1, &never);
+      }
+    } else if (warp == 1 && rank == 0) {
+      int b = 0, p = 0;
+      uint32_t ph = 0, pph = 0;
+      bool ok = true;
+      for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
+        const uint32_t idesc = idesc_e4m3(256, w.width);
+        for (int kb = 0; kb < a.n_blocks; ++kb) {
+          if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(lane & 1 ? &bar_full[b] : &bar_pfree[p],
+                                                           lane & 1 ? ph : pph ^ 1, abrt))))
+            break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t xd = smem_desc(smem_u32(ring + b * kWideStage));
+            const uint64_t wd = xd + (kFp8TileBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) tc_mma2_f8(tmem + p * 256, xd + kk * 2, wd + kk * 2, idesc, kk > 0);
+            tc_commit2(&bar_empty[b]);
+            tc_commit2(&bar_p[p]);
+          }
+          __syncwarp();
+          if (++b == S) b = 0, ph ^= 1;
+          if (++p == 2) p = 0, pph ^= 1;
+        }
+      }
+      if (*abrt) {  // let issued MMAs finish before TMEM is freed
+        volatile int never = 0;
+        if (elect_one()) tc_commit2(&bar_drain);
+        __syncwarp();
+        wait_bar(&bar_drain, 0, &never);
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideEpiRegs));
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
+    int p = 0;
+    uint32_t pph = 0;
+    bool ok = true;
+    pdl_wait();
+    for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
+      const int tok = rank * 128 + q * 32 + lane;  // of the unit
+      const int cols = w.width / 2, col0 = half * cols;
+      // (a lane without a token takes the last one's scales; its row is not stored)
+      const float* xs = a.xs + (size_t)(w.row + min(tok, w.ntok - 1)) * a.n_blocks;
+      const float* ws = a.ws + (size_t)(w.e * a.n_tiles + w.tile(col0)) * a.n_blocks;
+      float2 acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
+      // scales four blocks at a time, a group ahead of their use
+      float nx[4], nw[4];
+      auto fetch = [&](int kb) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = min(kb + j, a.n_blocks - 1);
+          nx[j] = __ldg(xs + k);
+          nw[j] = __ldg(ws + k);
+        }
+      };
+      fetch(0);
+      for (int kb4 = 0; ok && kb4 < a.n_blocks; kb4 += 4) {
+        float cx[4], cw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) cx[j] = nx[j], cw[j] = nw[j];
+        fetch(kb4 + 4);
+#pragma unroll
+        for (int j4 = 0; j4 < 4; ++j4) {
+          if (kb4 + j4 >= a.n_blocks) break;
+          if (!(ok = wait_bar_warp(&bar_p[p], pph, abrt))) break;
+          tc_fence_after();
+          const float s = cx[j4] * cw[j4];
+          uint32_t d[2][32];
+          const uint32_t at = lane_base + p * 256 + col0;
+          tmem_ld32(at, d[0]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i * 32 < cols) tmem_wait_ld();
+            if (i < 3 && (i + 1) * 32 < cols) tmem_ld32(at + (i + 1) * 32, d[(i + 1) & 1]);
+            if (i * 32 < cols) {
+              if (fabsf(s) >= 1e-37f && fabsf(s) <= 3e38f) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) fma2(acc[i * 16 + j], d[i & 1][2 * j], d[i & 1][2 * j + 1], s);
+              } else {  // the scales' product leaves fp32's range although a scaled sum need not
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  acc[i * 16 + j].x = fmaf(__uint_as_float(d[i & 1][2 * j]) * cx[j4], cw[j4], acc[i * 16 + j].x);
+                  acc[i * 16 + j].y = fmaf(__uint_as_float(d[i & 1][2 * j + 1]) * cx[j4], cw[j4], acc[i * 16 + j].y);
+                }
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_rank(&bar_pfree[p], 0);
+          if (++p == 2) p = 0, pph ^= 1;
+        }
+      }
+      if (!ok) break;
+      const int n0 = w.cu * 256 + w.piece * w.width + col0;
+      if (tok < w.ntok) {
+        const float* bias = a.out.bias ? a.out.bias + (size_t)w.e * a.N : nullptr;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int n = n0 + i * 32;
+          if (i * 32 < cols && n < a.N) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[2 * j] = acc[i * 16 + j].x, v[2 * j + 1] = acc[i * 16 + j].y;
+            if (bias) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (n + j < a.N) v[j] += __ldg(bias + n + j);
+            }
+            store_row32(a.out, (size_t)(w.row + tok) * a.N + n, a.N - n, vec, v);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abrt && threadIdx.x == 0) atomicOr(a.status, kStatusWaitTimeout);
+  // neither CTA frees TMEM or leaves while the other may still use its memory
+  __syncwarp();
+  cluster_arrive_relaxed();
+  cluster_wait();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc2(tmem, 512);
+  }
+}
+
+template <bool GROUPED>
+cudaError_t launch_wide(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cudaStream_t s) {
+  WideMaps m;
+  cudaError_t e = fp8_tensor_map(&m.x, xq, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)fp8_ld(a.K), 128);
+  if (e != cudaSuccess) return e;
+  m.w[0] = h.tm_w;
+  m.w[1] = h.tm_w64;
+  m.w[2] = h.tm_w32;
+  auto kern = fp8_wide_kernel<GROUPED>;
+  if ((e = allow_max_smem(reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
+  // the register split below must fit in what the block is launched with
+  static_assert(128 * kWideCtlRegs + 256 * kWideEpiRegs <= kWideThreads * 168, "register split");
+  static const int regs = [&] {
+    cudaFuncAttributes fa;
+    return cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern)) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs * kWideThreads < 128 * kWideCtlRegs + 256 * kWideEpiRegs) return cudaErrorLaunchOutOfResources;
+  const size_t esz = a.out.bf16 ? 2 : 4;
+  const uintptr_t al = reinterpret_cast<uintptr_t>(a.out.y) | (uintptr_t)(a.N * esz);
+  const int vec = al % 32 == 0 ? 32 : al % 16 == 0 ? 16 : 0;
+  return launch_pdl_cluster(kern, (unsigned)(h.num_sms / 2 * 2), kWideThreads, wide_smem(GROUPED ? a.n_experts : 0), 2,
+                            s, m, a, vec);
+}
+
 template <bool GROUPED>
 cudaError_t launch_mm(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cudaStream_t s) {
   // tokens an expert gets on average decide the block of tokens
@@ -589,7 +992,8 @@ cudaError_t launch_mm(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cuda
   if (per <= 16) return launch_skinny<16, GROUPED>(h, xq, a, s);
   if (per <= 32) return launch_skinny<32, GROUPED>(h, xq, a, s);
   if (per <= 64) return launch_skinny<64, GROUPED>(h, xq, a, s);
-  return launch_skinny<128, GROUPED>(h, xq, a, s);
+  if (per <= 128) return launch_skinny<128, GROUPED>(h, xq, a, s);
+  return launch_wide<GROUPED>(h, xq, a, s);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
