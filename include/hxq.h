@@ -384,7 +384,8 @@ void hxq_linear_destroy(hxq_linear_t h);
  *              float[M][ceil(K/128)]
  *  weights     uint8[N][K] and float[ceil(N/128)][ceil(K/128)]; the experts
  *              of one layer back to back
- * The products take any fp32 scales. The quantisers below write powers of
+ * The products take any fp32 scales (activation scale times weight scale being
+ * a normal fp32 number or 0: it is formed in fp32). The quantisers below write powers of
  * two: the smallest s with max |v| <= 448 s over the block, kept in
  * [2^-126, 2^120], and 1 for a block of zeros. Dividing by such a scale is
  * exact, so a byte is its value rounded once (to nearest, ties to even). NaN

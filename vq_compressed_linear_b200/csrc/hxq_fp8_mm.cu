@@ -82,6 +82,13 @@ __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];"
                ::"r"(map_to_rank(smem_u32(bar), rank)) : "memory");
 }
+// The same without ordering any memory but the tensor core's own (the
+// tcgen05 fences do that): a release at cluster scope waits for the thread's
+// stores and costs about a thousand cycles.
+__device__ __forceinline__ void mbar_signal_rank(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
+               ::"r"(map_to_rank(smem_u32(bar), rank)) : "memory");
+}
 // Waits, bounded at kWaitCycles (about 2 s): false, with *abort set, when the
 // limit passes or another thread of the CTA gave up. The limit is counted in
 // SM cycles: reading %globaltimer costs more than an ordinary wait here takes
@@ -549,6 +556,8 @@ cudaError_t cluster_fit(const void* kern, int device, size_t smem, const int** f
   return cudaSuccess;
 }
 
+cudaError_t fp8_out_map(CUtensorMap* tm, const Fp8Out& out, uint64_t N, uint64_t M);
+
 template <int BN, bool GROUPED>
 cudaError_t launch_skinny(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cudaStream_t s) {
   CUtensorMap tmx;
@@ -586,21 +595,35 @@ cudaError_t launch_skinny(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, 
 //
 // fp8_wide_kernel: D = x . W^T, lanes = tokens, columns = features, by pairs
 // of CTAs (tcgen05 cta_group::2): 256 tokens x 256 features a pair, each CTA
-// holding 128 of the tokens and 128 of the features' rows in shared memory
-// and its 128 tokens x 256 features of D in TMEM, twice. With tokens on the
+// with 128 of the tokens, in shared memory as in TMEM. With tokens on the
 // lanes a thread needs one scale per block of K (its token's times its
 // tile's), so adding P_b is one multiply-add per element.
 //
-// The units are (expert, 256 tokens, two tiles of W), token blocks fastest,
-// one after another on each pair; what does not fill the last round of all
-// pairs is cut into pieces of 128 or 64 features.
+// P_b has two buffers in TMEM. Eight warps read it, each 32 tokens x half the
+// features, in pieces of 32 columns: the next piece (of this block of K or
+// the next) loads while the last one is added, and a buffer is handed back
+// once its last piece has been read. (Halves of 128 features with an MMA and
+// buffers of their own were slower, 126 us against 113 for 2048 x 14336 x
+// 3584: an MMA of 128 columns reads its 256 tokens as often as one of 256.)
+//
+// The units are (expert, 256 tokens, two tiles of W), one after another on
+// each pair, in groups of 8 token blocks that walk the features together (so
+// that the pairs at work share both operands in L2); what does not fill the
+// last round of all pairs is cut into pieces of 128 or 64 features.
 
 constexpr int kWideTokens = 256;
-constexpr int kWideSlots = 6;
+constexpr int kWideSlots = 4;
+constexpr int kWideSc = 8;                     // ring of activation scales
+constexpr int kWideGroup = 8;                  // token blocks that walk the features together
 constexpr int kWideStage = 2 * kFp8TileBytes;  // 128 tokens and up to 128 features of one block of K
-constexpr int kWideThreads = 384;              // 4 warps of control, 8 that add and store
-constexpr int kWideCtlRegs = 40, kWideEpiRegs = 224;  // 128 * 40 + 256 * 224 <= 384 * 168
-constexpr size_t wide_smem(int E) { return 1024 + (size_t)kWideSlots * kWideStage + ranges_bytes(E); }
+constexpr int kWideAdders = 8;                 // warps that add and store: 32 tokens x half the features each
+constexpr int kWideThreads = 128 + 32 * kWideAdders;
+constexpr int kWideLaunchRegs = 168;           // a thread's at launch: 65536 / 384, a multiple of 8
+constexpr int kWideCtlRegs = 40, kWideAddRegs = 224;
+static_assert(128 * kWideCtlRegs + 32 * kWideAdders * kWideAddRegs <= kWideThreads * kWideLaunchRegs,
+              "register split: setmaxnreg draws on what the block was launched with");
+constexpr int kWideOut = 2 * 32 * 128;         // per adding warp: two pieces of 32 rows x 128 bytes on their way out
+constexpr size_t wide_smem(int E) { return 1024 + (size_t)kWideSlots * kWideStage + kWideAdders * kWideOut + ranges_bytes(E); }
 
 struct WideWalk {
   int item, step, items, full, cut, cu_n, e = 0;
@@ -634,8 +657,10 @@ struct WideWalk {
         first = R.first[e];
         rows = R.rows[e];
       }
-      cu = local / n_tb;
-      const int tb = local - cu * n_tb;
+      const int g = local / (kWideGroup * cu_n), in = local - g * kWideGroup * cu_n;
+      const int tbs = min(kWideGroup, n_tb - g * kWideGroup);
+      cu = in / tbs;
+      const int tb = g * kWideGroup + in - cu * tbs;
       row = first + tb * kWideTokens;
       ntok = min(kWideTokens, rows - tb * kWideTokens);
       const int have = 2 * cu + 1 < a.n_tiles ? 256 : 128;  // an odd last tile stands alone
@@ -643,8 +668,9 @@ struct WideWalk {
       if (piece * width < have) return true;
     }
   }
-  // Tile of W of the features from piece * width + off on.
+  // Tile of W and row in it of the piece's feature `off`.
   __device__ __forceinline__ int tile(int off) const { return 2 * cu + (piece * width + off) / kFp8Block; }
+  __device__ __forceinline__ int tile_row(int off) const { return (piece * width + off) % kFp8Block; }
 };
 
 __device__ __forceinline__ void tmem_alloc2(uint32_t* dst_smem, uint32_t ncols) {
@@ -682,84 +708,96 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, ui
       ::"r"(smem_u32(dst)), "l"(tmap), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
-  tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(v));
-  tmem_ld16(taddr + 16, *reinterpret_cast<uint32_t(*)[16]>(v + 16));
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
 }
 // (a0, a1) += (d0, d1) * (s, s)
 __device__ __forceinline__ void fma2(float2& a, uint32_t d0, uint32_t d1, float s) {
-  asm("{\n\t.reg .b64 x, y, z;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%0, %1};\n\t"
-      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "+f"(a.x), "+f"(a.y)
-      : "r"(d0), "r"(d1), "f"(s));
+  a = __ffma2_rn(make_float2(__uint_as_float(d0), __uint_as_float(d1)), make_float2(s, s), a);
 }
-
-// 32 consecutive outputs of one row; n of them exist. vec: bytes a store may
-// take (32, 16, or 0 for single elements).
-__device__ __forceinline__ void store_row32(const Fp8Out& o, size_t at, int n, int vec, const float (&v)[32]) {
-  if (o.bf16) {
-    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(o.y) + at;
-    if (vec && n >= 32) {
-      uint32_t w[16];
+// Outputs of a warp, one row per lane: w holds 128 bytes of it, columns n0 ..,
+// n of which exist. The rows go through `buf` (swizzled as the tensor map
+// has it: 16-byte chunk c of row r at c ^ (r & 7)) and, where all of them exist,
+// out as one TMA store that nobody waits for. Stored from the registers, or by a
+// bulk copy per lane, a tile's rows took 3500 cycles of 28 blocks' 22000.
+__device__ __forceinline__ void store_rows(const Fp8Out& o, const CUtensorMap* tmap, uint8_t* buf, int row, int N,
+                                           int n_rows, int n0, int n, int lane, bool tma, const uint32_t (&w)[32]) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      if (vec == 32) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 8)
-          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                       ::"l"(p + 2 * j), "r"(w[j]), "r"(w[j + 1]), "r"(w[j + 2]), "r"(w[j + 3]), "r"(w[j + 4]),
-                         "r"(w[j + 5]), "r"(w[j + 6]), "r"(w[j + 7])
-                       : "memory");
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; j += 4)
-          *reinterpret_cast<uint4*>(p + 2 * j) = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) p[j] = __float2bfloat16_rn(v[j]);
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(buf + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  // (a box reaches past n only where y ends)
+  if (tma && n_rows >= 32 && (n >= 128 / (o.bf16 ? 2 : 4) || n0 + n == N)) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];"
+                   ::"l"(tmap), "r"(n0), "r"(row), "r"(smem_u32(buf))
+                   : "memory");
     }
   } else {
-    float* p = static_cast<float*>(o.y) + at;
-    if (vec && n >= 32) {
-      if (vec == 32) {
+    __syncwarp();
+    const int esz = o.bf16 ? 2 : 4;
+    n = min(n, 128 / esz);
+    uint8_t* y = static_cast<uint8_t*>(o.y) + ((size_t)row * N + n0) * esz;
+    if (tma) {  // rows of whole 16-byte pieces
+      const int c = lane & 7;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8)
-          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                       ::"l"(p + j), "f"(v[j]), "f"(v[j + 1]), "f"(v[j + 2]), "f"(v[j + 3]), "f"(v[j + 4]),
-                         "f"(v[j + 5]), "f"(v[j + 6]), "f"(v[j + 7])
-                       : "memory");
-      } else {
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(p + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        if (r < n_rows && c * 16 < n * esz)
+          *reinterpret_cast<uint4*>(y + (size_t)r * N * esz + c * 16) =
+              *reinterpret_cast<const uint4*>(buf + r * 128 + ((c ^ (r & 7)) << 4));
       }
     } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) p[j] = v[j];
+#pragma unroll 4
+      for (int r = 0; r < min(n_rows, 32); ++r)
+        for (int b = lane * esz; b < n * esz; b += 32 * esz) {
+          const uint8_t* src = buf + r * 128 + (((b >> 4) ^ (r & 7)) << 4) + (b & 15);
+          uint8_t* dst = y + (size_t)r * N * esz + b;
+          if (o.bf16)
+            *reinterpret_cast<uint16_t*>(dst) = *reinterpret_cast<const uint16_t*>(src);
+          else
+            *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
+        }
     }
+    __syncwarp();
   }
+  if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// The pieces that this warp stored before the last `left` have left `buf`.
+template <int LEFT>
+__device__ __forceinline__ void stores_read(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory");
+  __syncwarp();
 }
 
 struct WideMaps {
   CUtensorMap x;      // 128 tokens
+  CUtensorMap y;      // 32 rows x 128 bytes
   CUtensorMap w[3];   // 128, 64, 32 rows of a tile
 };
 
 template <bool GROUPED>
 __global__ void __launch_bounds__(kWideThreads, 1)
-fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int vec) {
+fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
   constexpr int S = kWideSlots;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
-  const Ranges R = ranges_at(ring + S * kWideStage, a.n_experts);
+  uint8_t* outs = ring + S * kWideStage;
+  const Ranges R = ranges_at(outs + kWideAdders * kWideOut, a.n_experts);
   // full and pfree are used in the leading CTA only; empty and p arrive in both
   __shared__ uint64_t bar_full[S], bar_empty[S], bar_p[2], bar_pfree[2], bar_drain;
+  __shared__ uint64_t bar_s[kWideSc], bar_sfree[kWideSc];
+  __shared__ float sc[kWideSc][128 + 2];  // a block's activation scales, then the two tiles' scales
   __shared__ uint32_t tmem_sh;
   __shared__ int abort_sh;
 
@@ -776,7 +814,11 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int vec) {
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_p[i], 1);
-      mbar_init(&bar_pfree[i], 16);
+      mbar_init(&bar_pfree[i], 2 * kWideAdders);
+    }
+    for (int i = 0; i < kWideSc; ++i) {
+      mbar_init(&bar_s[i], 32);
+      mbar_init(&bar_sfree[i], kWideAdders);
     }
     mbar_init(&bar_drain, 1);
     abort_sh = 0;
@@ -805,11 +847,10 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int vec) {
       bool ok = true;
       pdl_wait();
       for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
-        // this CTA's rows of W: a tile of its own, or its half of the piece
-        const int rows = w.width / 2;
+        // of the piece's features each CTA holds one half
+        const int rows = w.width / 2, off = rank * rows;
         const CUtensorMap* tw = rows == 128 ? &maps.w[0] : rows == 64 ? &maps.w[1] : &maps.w[2];
-        const int off = rank * rows;
-        const int w0 = (w.e * a.n_tiles + w.tile(off)) * a.n_blocks * kFp8Block + (w.piece * w.width + off) % kFp8Block;
+        const int w0 = (w.e * a.n_tiles + w.tile(off)) * a.n_blocks * kFp8Block + w.tile_row(off);
         const int x0 = w.row + rank * 128;
         for (int kb = 0; kb < a.n_blocks; ++kb) {
           if (!(ok = wait_bar_warp(&bar_empty[b], ph ^ 1, abrt))) break;
@@ -836,17 +877,15 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int vec) {
       for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
         const uint32_t idesc = idesc_e4m3(256, w.width);
         for (int kb = 0; kb < a.n_blocks; ++kb) {
-          if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(lane & 1 ? &bar_full[b] : &bar_pfree[p],
-                                                           lane & 1 ? ph : pph ^ 1, abrt))))
-            break;
+          if (!(ok = wait_bar_warp(lane & 1 ? &bar_full[b] : &bar_pfree[p], lane & 1 ? ph : pph ^ 1, abrt))) break;
           tc_fence_after();
           if (elect_one()) {
             const uint64_t xd = smem_desc(smem_u32(ring + b * kWideStage));
             const uint64_t wd = xd + (kFp8TileBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) tc_mma2_f8(tmem + p * 256, xd + kk * 2, wd + kk * 2, idesc, kk > 0);
-            tc_commit2(&bar_empty[b]);
             tc_commit2(&bar_p[p]);
+            tc_commit2(&bar_empty[b]);
           }
           __syncwarp();
           if (++b == S) b = 0, ph ^= 1;
@@ -859,93 +898,109 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int vec) {
         __syncwarp();
         wait_bar(&bar_drain, 0, &never);
       }
+    } else if (warp == 3) {
+      int sp = 0;
+      uint32_t sph = 0;
+      bool ok = true;
+      pdl_wait();
+      for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
+        const float* ws = a.ws + (size_t)(w.e * a.n_tiles + w.tile(lane * w.width / 2)) * a.n_blocks;
+        for (int kb = 0; kb < a.n_blocks; ++kb) {
+          if (!(ok = wait_bar_warp(&bar_sfree[sp], sph ^ 1, abrt))) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = i * 32 + lane, tok = rank * 128 + t;  // (rows past the tokens are never stored)
+            if (tok < w.ntok) cp_async4(&sc[sp][t], a.xs + (size_t)(w.row + tok) * a.n_blocks + kb);
+          }
+          if (lane < 2) cp_async4(&sc[sp][128 + lane], ws + kb);
+          cp_async_arrive(&bar_s[sp]);
+          if (++sp == kWideSc) sp = 0, sph ^= 1;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideEpiRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideAddRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
-    int p = 0;
-    uint32_t pph = 0;
+    int p = 0, sp = 0;
+    uint32_t pph = 0, sph = 0;
     bool ok = true;
     pdl_wait();
     for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
-      const int tok = rank * 128 + q * 32 + lane;  // of the unit
       const int cols = w.width / 2, col0 = half * cols;
-      // (a lane without a token takes the last one's scales; its row is not stored)
-      const float* xs = a.xs + (size_t)(w.row + min(tok, w.ntok - 1)) * a.n_blocks;
-      const float* ws = a.ws + (size_t)(w.e * a.n_tiles + w.tile(col0)) * a.n_blocks;
       float2 acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
-      // scales four blocks at a time, a group ahead of their use
-      float nx[4], nw[4];
-      auto fetch = [&](int kb) {
+      for (int kb = 0; kb < a.n_blocks; ++kb) {
+        if (!(ok = wait_bar_warp(lane & 1 ? &bar_p[p] : &bar_s[sp], lane & 1 ? pph : sph, abrt))) break;
+        tc_fence_after();
+        const uint32_t at = lane_base + p * 256 + col0;
+        const float s = sc[sp][q * 32 + lane] * sc[sp][128 + half];
+        uint32_t d[64];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = min(kb + j, a.n_blocks - 1);
-          nx[j] = __ldg(xs + k);
-          nw[j] = __ldg(ws + k);
-        }
-      };
-      fetch(0);
-      for (int kb4 = 0; ok && kb4 < a.n_blocks; kb4 += 4) {
-        float cx[4], cw[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) cx[j] = nx[j], cw[j] = nw[j];
-        fetch(kb4 + 4);
-#pragma unroll
-        for (int j4 = 0; j4 < 4; ++j4) {
-          if (kb4 + j4 >= a.n_blocks) break;
-          if (!(ok = wait_bar_warp(&bar_p[p], pph, abrt))) break;
-          tc_fence_after();
-          const float s = cx[j4] * cw[j4];
-          uint32_t d[2][32];
-          const uint32_t at = lane_base + p * 256 + col0;
-          tmem_ld32(at, d[0]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (i * 32 < cols) tmem_wait_ld();
-            if (i < 3 && (i + 1) * 32 < cols) tmem_ld32(at + (i + 1) * 32, d[(i + 1) & 1]);
-            if (i * 32 < cols) {
-              if (fabsf(s) >= 1e-37f && fabsf(s) <= 3e38f) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) fma2(acc[i * 16 + j], d[i & 1][2 * j], d[i & 1][2 * j + 1], s);
-              } else {  // the scales' product leaves fp32's range although a scaled sum need not
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  acc[i * 16 + j].x = fmaf(__uint_as_float(d[i & 1][2 * j]) * cx[j4], cw[j4], acc[i * 16 + j].x);
-                  acc[i * 16 + j].y = fmaf(__uint_as_float(d[i & 1][2 * j + 1]) * cx[j4], cw[j4], acc[i * 16 + j].y);
-                }
+        for (int i = 0; i < 2; ++i) {
+          if (i * 64 < cols) {
+            tmem_ld32(at + i * 64, d);
+            tmem_ld32(at + i * 64 + 32, d + 32);  // (columns past a narrow width hold nothing that is stored)
+            tmem_wait_ld();
+            if (i == 1 || cols <= 64) {  // the last read of this buffer and of its scales
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_signal_rank(&bar_pfree[p], 0);
+                mbar_arrive(&bar_sfree[sp]);
               }
             }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) fma2(acc[i * 32 + j], d[2 * j], d[2 * j + 1], s);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_rank(&bar_pfree[p], 0);
-          if (++p == 2) p = 0, pph ^= 1;
         }
+        if (++p == 2) p = 0, pph ^= 1;
+        if (++sp == kWideSc) sp = 0, sph ^= 1;
       }
       if (!ok) break;
       const int n0 = w.cu * 256 + w.piece * w.width + col0;
-      if (tok < w.ntok) {
-        const float* bias = a.out.bias ? a.out.bias + (size_t)w.e * a.N : nullptr;
+      const int n = min(cols, a.N - n0), n_rows = w.ntok - (rank * 128 + q * 32);
+      if (n <= 0 || n_rows <= 0) continue;
+      const int row = w.row + rank * 128 + q * 32;
+      uint8_t* buf = outs + (warp - 4) * kWideOut;
+      if (a.out.bias) {
+        const float* bias = a.out.bias + (size_t)w.e * a.N + n0;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+          if (2 * j < n) acc[j].x += __ldg(bias + 2 * j);
+          if (2 * j + 1 < n) acc[j].y += __ldg(bias + 2 * j + 1);
+        }
+      }
+      uint32_t v[32];
+      stores_read<0>(lane);
+      if (a.out.bf16) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (i * 64 >= n) break;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const __nv_bfloat162 t = __floats2bfloat162_rn(acc[i * 32 + j].x, acc[i * 32 + j].y);
+            v[j] = *reinterpret_cast<const uint32_t*>(&t);
+          }
+          store_rows(a.out, &maps.y, buf + i * 4096, row, a.N, n_rows, n0 + i * 64, n - i * 64, lane, tma_out, v);
+        }
+      } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int n = n0 + i * 32;
-          if (i * 32 < cols && n < a.N) {
-            float v[32];
+          if (i * 32 >= n) break;
+          if (i >= 2) stores_read<1>(lane);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[2 * j] = acc[i * 16 + j].x, v[2 * j + 1] = acc[i * 16 + j].y;
-            if (bias) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (n + j < a.N) v[j] += __ldg(bias + n + j);
-            }
-            store_row32(a.out, (size_t)(w.row + tok) * a.N + n, a.N - n, vec, v);
+          for (int j = 0; j < 16; ++j) {
+            v[2 * j] = __float_as_uint(acc[i * 16 + j].x);
+            v[2 * j + 1] = __float_as_uint(acc[i * 16 + j].y);
           }
+          store_rows(a.out, &maps.y, buf + (i & 1) * 4096, row, a.N, n_rows, n0 + i * 32, n - i * 32, lane, tma_out, v);
         }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the rows have arrived
   }
 
   tc_fence_before();
@@ -971,18 +1026,19 @@ cudaError_t launch_wide(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cu
   m.w[2] = h.tm_w32;
   auto kern = fp8_wide_kernel<GROUPED>;
   if ((e = allow_max_smem(reinterpret_cast<const void*>(kern))) != cudaSuccess) return e;
-  // the register split below must fit in what the block is launched with
-  static_assert(128 * kWideCtlRegs + 256 * kWideEpiRegs <= kWideThreads * 168, "register split");
+  // (the register split assumes what the block is launched with)
   static const int regs = [&] {
     cudaFuncAttributes fa;
     return cudaFuncGetAttributes(&fa, reinterpret_cast<const void*>(kern)) == cudaSuccess ? fa.numRegs : 0;
   }();
-  if (regs * kWideThreads < 128 * kWideCtlRegs + 256 * kWideEpiRegs) return cudaErrorLaunchOutOfResources;
+  if (regs < kWideLaunchRegs) return cudaErrorLaunchOutOfResources;
+  // whole pieces of y leave by TMA where its rows allow a tensor map
   const size_t esz = a.out.bf16 ? 2 : 4;
-  const uintptr_t al = reinterpret_cast<uintptr_t>(a.out.y) | (uintptr_t)(a.N * esz);
-  const int vec = al % 32 == 0 ? 32 : al % 16 == 0 ? 16 : 0;
+  const int tma_out = (reinterpret_cast<uintptr_t>(a.out.y) | (uintptr_t)(a.N * esz)) % 16 == 0;
+  m.y = m.x;
+  if (tma_out && (e = fp8_out_map(&m.y, a.out, (uint64_t)a.N, (uint64_t)a.M)) != cudaSuccess) return e;
   return launch_pdl_cluster(kern, (unsigned)(h.num_sms / 2 * 2), kWideThreads, wide_smem(GROUPED ? a.n_experts : 0), 2,
-                            s, m, a, vec);
+                            s, m, a, tma_out);
 }
 
 template <bool GROUPED>
@@ -1006,6 +1062,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   }();
   return fn;
+}
+
+// y [M][N], boxes of 32 rows x 128 bytes in the 128-byte swizzle.
+cudaError_t fp8_out_map(CUtensorMap* tm, const Fp8Out& out, uint64_t N, uint64_t M) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint32_t esz = out.bf16 ? 2 : 4;
+  cuuint64_t dims[2] = {N, M};
+  cuuint64_t strides[1] = {N * esz};
+  cuuint32_t box[2] = {128 / esz, 32};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(tm, out.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, out.y, dims, strides,
+            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
 }
 
 }  // namespace
