@@ -452,70 +452,90 @@ def encode(W, mode, codebook, threshold, max_sidecar=None, stream=None):
 
 # ---- 8-bit-float layers --------------------------------------------------------
 # Tensors are checked here for what the C ABI cannot see: shape, type,
-# contiguity and device. A mismatch raises HXQError with HXQ_EINVAL.
+# contiguity and device. A mismatch raises HXQError with HXQ_EINVAL. These
+# wrappers sit in the path of a decode step: they call the library directly,
+# take outputs that exist already, and build no message unless they raise.
 
-def _want(cond, what: str) -> None:
-    if not cond:
-        raise HXQError(HXQ_EINVAL, what)
+class _Torch:
+    """What the wrappers use of torch, looked up once (importing this module
+    does not import torch)."""
 
-
-_types: dict = {}
-
-
-def _fp8_types() -> dict:
-    """torch dtype -> HXQ_TYPE_*, and the 8-bit dtypes (filled at first use:
-    importing this module does not import torch)."""
-    if not _types:
+    def __init__(self):
         import torch
-        _types.update({torch.float32: HXQ_TYPE_F32, torch.bfloat16: HXQ_TYPE_BF16, "f32": torch.float32,
-                       "bf16": torch.bfloat16, "q": torch.float8_e4m3fn, "q8": (torch.float8_e4m3fn, torch.uint8),
-                       "i32": torch.int32, "empty": torch.empty, "device": torch.cuda.current_device})
-    return _types
+        self.f32, self.bf16, self.i32 = torch.float32, torch.bfloat16, torch.int32
+        self.q, self.q8 = torch.float8_e4m3fn, (torch.float8_e4m3fn, torch.uint8)
+        self.code = {torch.float32: HXQ_TYPE_F32, torch.bfloat16: HXQ_TYPE_BF16}
+        self.empty = torch.empty
+        self.device = torch.cuda.current_device
+        # the current stream's handle without building a Stream object
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _input(t, what: str):
-    """A 2D CUDA tensor of float32 or bfloat16 on the current device, contiguous; its HXQ_TYPE_*."""
-    ty = _fp8_types()
-    code = ty.get(t.dtype)
-    _want(code is not None and t.is_cuda and t.dim() >= 1 and t.shape[-1] > 0 and t.get_device() == ty["device"](),
-          f"{what}: a float32 or bfloat16 tensor on the current CUDA device")
-    return t if t.is_contiguous() else t.contiguous(), code
+_torch = None
 
 
-def _output(t, shape, dtypes, device, what: str):
-    """`t`, checked, or a new tensor of that shape (of the first dtype)."""
+def _t() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _refuse(what: str):
+    raise HXQError(HXQ_EINVAL, what)
+
+
+def _raw(stream, device: int):
+    return _torch.raw_stream(device) if stream is None else int(getattr(stream, "cuda_stream", stream))
+
+
+def _input(t, dims: int, what: str):
+    """`t` contiguous and its HXQ_TYPE_*: float32 or bfloat16 on the current CUDA device."""
+    code = _t().code.get(t.dtype)
+    if code is None or not t.is_cuda or t.dim() != dims or t.get_device() != _torch.device():
+        _refuse(f"{what}: a {dims}D float32 or bfloat16 tensor on the current CUDA device")
+    return (t if t.is_contiguous() else t.contiguous()), code
+
+
+def _output(t, shape, dtype, device: int, what: str):
+    """`t`, checked, or a new tensor of that shape and type."""
     if t is None:
-        return _fp8_types()["empty"](shape, dtype=dtypes[0], device=device)
-    _want(t.shape == shape and t.dtype in dtypes and t.is_contiguous() and t.device == device,
-          f"{what}: a contiguous {dtypes[0]} tensor of shape {tuple(shape)} on {device}")
+        return _torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        _refuse(f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {device}")
     return t
 
 
-def _quantized(rows, cols, q, scales, device, what):
-    ty = _fp8_types()
-    return (_output(q, (rows, (cols + 15) // 16 * 16), ty["q8"], device, what + ": q"),
-            _output(scales, (rows, (cols + 127) // 128), (ty["f32"],), device, what + ": scales"))
+def _bytes(t, shape, device: int, what: str):
+    """As _output for 8-bit values, which may also come as uint8."""
+    return _output(t, shape, _torch.q if t is None or t.dtype is not _torch.q8[1] else t.dtype, device, what)
 
 
 def fp8_quantize(x, q=None, scales=None, stream=None):
     """x [M, K] (float32 or bfloat16 CUDA) as an 8-bit activation. Returns
     (q float8_e4m3fn [M, K rounded up to 16], scales float32 [M, ceil(K / 128)])."""
-    x, code = _input(x, "fp8_quantize")
-    _want(x.dim() == 2, "fp8_quantize: x is [M, K]")
-    rows, cols = x.shape
-    q, scales = _quantized(rows, cols, q, scales, x.device, "fp8_quantize")
-    hxq_fp8_quantize(x, code, rows, cols, q, scales, stream)
+    x, code = _input(x, 2, "fp8_quantize")
+    (rows, cols), dev = x.shape, x.get_device()
+    q = _bytes(q, (rows, (cols + 15) // 16 * 16), dev, "fp8_quantize: q")
+    scales = _output(scales, (rows, (cols + 127) // 128), _torch.f32, dev, "fp8_quantize: scales")
+    _check(lib.hxq_fp8_quantize(x.data_ptr(), code, rows, cols, q.data_ptr(), scales.data_ptr(), _raw(stream, dev)),
+           "hxq_fp8_quantize")
     return q, scales
 
 
 def fp8_swiglu(gate_up, q=None, scales=None, stream=None):
     """silu(gate) * up of gate_up [M, 2 K] (gate first) as an 8-bit
     activation [M, K]; returns (q, scales) as fp8_quantize."""
-    x, code = _input(gate_up, "fp8_swiglu")
-    _want(x.dim() == 2 and x.shape[1] % 2 == 0, "fp8_swiglu: gate_up is [M, 2 K]")
-    rows, cols = x.shape[0], x.shape[1] // 2
-    q, scales = _quantized(rows, cols, q, scales, x.device, "fp8_swiglu")
-    hxq_fp8_swiglu(x, code, rows, cols, q, scales, stream)
+    x, code = _input(gate_up, 2, "fp8_swiglu")
+    (rows, both), dev = x.shape, x.get_device()
+    if both % 2:
+        _refuse("fp8_swiglu: gate_up is [M, 2 K]")
+    cols = both // 2
+    q = _bytes(q, (rows, (cols + 15) // 16 * 16), dev, "fp8_swiglu: q")
+    scales = _output(scales, (rows, (cols + 127) // 128), _torch.f32, dev, "fp8_swiglu: scales")
+    _check(lib.hxq_fp8_swiglu(x.data_ptr(), code, rows, cols, q.data_ptr(), scales.data_ptr(), _raw(stream, dev)),
+           "hxq_fp8_swiglu")
     return q, scales
 
 
@@ -523,14 +543,12 @@ def fp8_encode(W, q=None, scales=None, stream=None):
     """Weights [N, K] or [E, N, K] (float32 or bfloat16 CUDA) as 8-bit values
     of the same shape and scales [(E,) ceil(N / 128), ceil(K / 128)]: what
     Fp8Linear takes."""
-    W, code = _input(W, "fp8_encode")
-    _want(W.dim() in (2, 3) and W.numel() > 0, "fp8_encode: W is [N, K] or [E, N, K]")
-    ty = _fp8_types()
-    N, K = W.shape[-2:]
-    q = _output(q, W.shape, ty["q8"], W.device, "fp8_encode: q")
-    scales = _output(scales, (*W.shape[:-2], (N + 127) // 128, (K + 127) // 128), (ty["f32"],), W.device,
-                     "fp8_encode: scales")
-    hxq_fp8_encode(W, code, W.shape[0] if W.dim() == 3 else 1, N, K, q, scales, stream)
+    W, code = _input(W, 3 if W.dim() == 3 else 2, "fp8_encode")
+    dev, (N, K) = W.get_device(), W.shape[-2:]
+    q = _bytes(q, W.shape, dev, "fp8_encode: q")
+    scales = _output(scales, (*W.shape[:-2], (N + 127) // 128, (K + 127) // 128), _torch.f32, dev, "fp8_encode: scales")
+    _check(lib.hxq_fp8_encode(W.data_ptr(), code, W.shape[0] if W.dim() == 3 else 1, N, K, q.data_ptr(),
+                              scales.data_ptr(), _raw(stream, dev)), "hxq_fp8_encode")
     return q, scales
 
 
@@ -544,32 +562,39 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=Non
     given of y and q (q if neither is). sum_out receives t (it may be the
     residual itself; a new tensor if there is a residual and none is given).
     Returns (q, scales, y, sum), None for what was not asked for."""
-    x, xt = _input(x, "rmsnorm")
-    _want(x.dim() == 2, "rmsnorm: x is [M, K]")
-    ty = _fp8_types()
-    rows, cols = x.shape
-    dev = x.device
+    x, xt = _input(x, 2, "rmsnorm")
+    T = _torch
+    shape, dev = x.shape, x.get_device()
+    rows, cols = shape
     if want is None:
-        want = ("q" if q is not None or y is None else "") + ("y" if y is not None else "")
-    _want(want in ("q", "y", "qy", "yq"), "rmsnorm: want is 'q', 'y' or 'qy'")
+        want_y, want_q = y is not None, q is not None or y is None
+    else:
+        want_y, want_q = "y" in want, "q" in want
+        if want not in ("q", "y", "qy", "yq") or (y is not None and not want_y) or (q is not None and not want_q):
+            _refuse("rmsnorm: want is 'q', 'y' or 'qy', and covers the outputs that are given")
+    rp = sp = wp = yp = qp = cp = None
     rt = xt
     if residual is not None:
-        residual, rt = _input(residual, "rmsnorm: residual")
-        _want(residual.shape == x.shape and residual.device == dev, "rmsnorm: residual has the shape of x")
-        sum_out = _output(sum_out, x.shape, (residual.dtype,), dev, "rmsnorm: sum_out")
-    else:
-        _want(sum_out is None, "rmsnorm: sum_out without a residual")
+        residual, rt = _input(residual, 2, "rmsnorm: residual")
+        if residual.shape != shape:
+            _refuse("rmsnorm: residual has the shape of x")
+        sum_out = _output(sum_out, shape, residual.dtype, dev, "rmsnorm: sum_out")
+        rp, sp = residual.data_ptr(), sum_out.data_ptr()
+    elif sum_out is not None:
+        _refuse("rmsnorm: sum_out without a residual")
     if weight is not None:
-        _output(weight, (cols,), (ty["f32"],), dev, "rmsnorm: weight")
-    if "q" in want:
-        q, scales = _quantized(rows, cols, q, scales, dev, "rmsnorm")
-    else:
-        _want(q is None and scales is None, "rmsnorm: q without 'q' in want")
-    if "y" in want:
-        y = _output(y, x.shape, (ty["bf16"],), dev, "rmsnorm: y")
-    else:
-        _want(y is None, "rmsnorm: y without 'y' in want")
-    hxq_rmsnorm(x, xt, residual, sum_out, rt, weight, eps, rows, cols, y, q, scales, stream)
+        wp = _output(weight, (cols,), T.f32, dev, "rmsnorm: weight").data_ptr()
+    if want_q:
+        q = _bytes(q, (rows, (cols + 15) // 16 * 16), dev, "rmsnorm: q")
+        scales = _output(scales, (rows, (cols + 127) // 128), T.f32, dev, "rmsnorm: scales")
+        qp, cp = q.data_ptr(), scales.data_ptr()
+    elif scales is not None:
+        _refuse("rmsnorm: scales without q")
+    if want_y:
+        y = _output(y, shape, T.bf16, dev, "rmsnorm: y")
+        yp = y.data_ptr()
+    _check(lib.hxq_rmsnorm(x.data_ptr(), xt, rp, sp, rt, wp, eps, rows, cols, yp, qp, cp, _raw(stream, dev)),
+           "hxq_rmsnorm")
     return q, scales, y, sum_out
 
 
@@ -581,14 +606,15 @@ class Fp8Linear:
     """
 
     def __init__(self, W, scales):
-        ty = _fp8_types()
-        _want(W.dim() in (2, 3) and W.numel() > 0 and W.dtype in ty["q8"], "Fp8Linear: W is [N, K] or [E, N, K], 8 bits")
+        T = _t()
+        if W.dim() not in (2, 3) or W.numel() == 0 or W.dtype not in T.q8:
+            _refuse("Fp8Linear: W is [N, K] or [E, N, K], 8 bits")
         self.grouped = W.dim() == 3
         self.E = int(W.shape[0]) if self.grouped else 1
         self.N, self.K = int(W.shape[-2]), int(W.shape[-1])
         self._ld, self._kb = (self.K + 15) // 16 * 16, (self.K + 127) // 128
-        _want(scales.dtype == ty["f32"] and scales.shape == (*W.shape[:-2], (self.N + 127) // 128, self._kb),
-              "Fp8Linear: scales are float32, one per 128 x 128 block")
+        if scales.dtype is not T.f32 or scales.shape != (*W.shape[:-2], (self.N + 127) // 128, self._kb):
+            _refuse("Fp8Linear: scales are float32, one per 128 x 128 block")
         self.handle = hxq_fp8_create(W.contiguous(), scales.contiguous(), self.E, self.N, self.K)
 
     @classmethod
@@ -596,28 +622,27 @@ class Fp8Linear:
         """From float32 or bfloat16 CUDA weights [N, K] or [E, N, K]."""
         return cls(*fp8_encode(W))
 
-    def _run(self, xq, xs, offsets, bias, out_dtype, y, stream):
-        ty = _fp8_types()
-        M, dev = xq.shape[0], xq.device
-        _want(xq.shape == (M, self._ld) and xq.dtype in ty["q8"] and xq.is_contiguous() and
-              dev.index == ty["device"](), f"Fp8Linear: xq is a contiguous 8-bit tensor [M, {self._ld}] on the current "
-              "CUDA device")
-        _output(xs, (M, self._kb), (ty["f32"],), dev, "Fp8Linear: xs")
+    def _args(self, xq, xs, bias, out_dtype, y, stream):
+        T = _torch
+        M, dev = xq.shape[0], xq.get_device()
+        if dev < 0:
+            _refuse("Fp8Linear: xq is a CUDA tensor")
+        _bytes(xq, (M, self._ld), dev, "Fp8Linear: xq")
+        _output(xs, (M, self._kb), T.f32, dev, "Fp8Linear: xs")
+        bp = None
         if bias is not None:
-            _output(bias, (self.E, self.N) if self.grouped else (self.N,), (ty["f32"],), dev, "Fp8Linear: bias")
-        y = _output(y, (M, self.N), (ty["bf16" if out_dtype == HXQ_OUT_BF16 else "f32"],), dev, "Fp8Linear: y")
-        if offsets is None:
-            hxq_fp8_forward(self.handle, xq, xs, bias, y, out_dtype, M, stream)
-        else:
-            _output(offsets, (self.E + 1,), (ty["i32"],), dev, "Fp8Linear: offsets")
-            hxq_fp8_forward_grouped(self.handle, xq, xs, offsets, bias, y, out_dtype, M, stream)
-        return y
+            bp = _output(bias, (self.E, self.N) if self.grouped else (self.N,), T.f32, dev, "Fp8Linear: bias").data_ptr()
+        y = _output(y, (M, self.N), T.bf16 if out_dtype == HXQ_OUT_BF16 else T.f32, dev, "Fp8Linear: y")
+        return M, xq.data_ptr(), xs.data_ptr(), bp, y, _raw(stream, dev)
 
     def forward(self, xq, xs, bias=None, out_dtype=HXQ_OUT_F32, y=None, stream=None):
         """y = x . W^T (+ bias [N]) as float32, or as bfloat16 with
         out_dtype=HXQ_OUT_BF16."""
-        _want(not self.grouped, "Fp8Linear: forward_grouped runs the experts")
-        return self._run(xq, xs, None, bias, out_dtype, y, stream)
+        if self.grouped:
+            _refuse("Fp8Linear: forward_grouped runs the experts")
+        M, xp, sp, bp, y, st = self._args(xq, xs, bias, out_dtype, y, stream)
+        _check(lib.hxq_fp8_forward(self.handle, xp, sp, bp, y.data_ptr(), out_dtype, M, st), "hxq_fp8_forward")
+        return y
 
     __call__ = forward
 
@@ -625,8 +650,13 @@ class Fp8Linear:
         """Rows offsets[e] .. offsets[e + 1] - 1 (int32 CUDA [E + 1]) times
         expert e's weights (+ bias [E, N]). Rows outside all of them are left
         as they were in y (unwritten in a new y)."""
-        _want(self.grouped and offsets is not None, "Fp8Linear: forward_grouped takes weights [E, N, K] and offsets")
-        return self._run(xq, xs, offsets, bias, out_dtype, y, stream)
+        if not self.grouped or offsets is None:
+            _refuse("Fp8Linear: forward_grouped takes weights [E, N, K] and offsets")
+        M, xp, sp, bp, y, st = self._args(xq, xs, bias, out_dtype, y, stream)
+        op = _output(offsets, (self.E + 1,), _torch.i32, xq.get_device(), "Fp8Linear: offsets").data_ptr()
+        _check(lib.hxq_fp8_forward_grouped(self.handle, xp, sp, op, bp, y.data_ptr(), out_dtype, M, st),
+               "hxq_fp8_forward_grouped")
+        return y
 
     def check(self) -> None:
         hxq_fp8_check(self.handle)
