@@ -219,27 +219,30 @@ struct Walk {
 
 // ---- few tokens ---------------------------------------------------------------
 
-constexpr int kSkThreads = 256;
 template <int BN>
 struct Sk {
-  static constexpr int kPer = BN <= 64 ? 2 : 1;  // blocks of K per stage
+  static constexpr int kPer = 2;                 // blocks of K per stage
+  // groups of four adding warps, each with every other 16 columns: one group
+  // alone takes 1000 cycles for a stage of 64 columns, the MMAs 450
+  static constexpr int kGroups = BN >= 32 ? 2 : 1;
+  static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kXBytes = BN * kFp8Block;
   static constexpr int kStage = kPer * (kFp8TileBytes + kXBytes);
-  static constexpr int kSlots = BN <= 16 ? 5 : BN <= 32 ? 4 : BN <= 64 ? 3 : 4;  // operands in, P out (TMEM)
+  static constexpr int kSlots = BN <= 16 ? 5 : BN <= 32 ? 4 : 3;               // operands in, P out (TMEM)
   static constexpr int kUsed = kSlots * kPer * BN;
-  static constexpr int kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;    // allocated: a power of two
-  static constexpr int kSc = 8;                                                  // ring of activation scales
+  static constexpr int kCols = kUsed <= 256 ? 256 : 512;                       // allocated: a power of two
+  static constexpr int kSc = 8;                                                // ring of activation scales
   static constexpr int kMaxCluster = 16;
-  static constexpr int kRecv = (BN + kMaxCluster) * kFp8Block * 4;               // cluster sums
+  static constexpr int kRecv = (BN + kMaxCluster) * kFp8Block * 4;             // cluster sums
   static constexpr size_t smem(int E) { return 1024 + (size_t)kSlots * kStage + kRecv + ranges_bytes(E); }
 };
 
 template <int BN, bool GROUPED>
-__global__ void __launch_bounds__(kSkThreads, 1)
+__global__ void __launch_bounds__(Sk<BN>::kThreads, 1)
 fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant__ CUtensorMap tmx, MmArgs a,
                   int cluster, int own, int own_inv) {
   using C = Sk<BN>;
-  constexpr int S = C::kSlots, KP = C::kPer, SC = C::kSc;
+  constexpr int S = C::kSlots, KP = C::kPer, SC = C::kSc, G = C::kGroups;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem + ((1024u - (smem_u32(smem) & 1023u)) & 1023u);
   float* recv = reinterpret_cast<float*>(ring + S * C::kStage);  // [source rank][own column][128 rows]
@@ -287,15 +290,15 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
     if (elect_one()) {
       for (int i = 0; i < S; ++i) {
         mbar_init(&bar_p[i], 1);
-        mbar_init(&bar_pfree[i], 4);
+        mbar_init(&bar_pfree[i], 4 * G);
       }
       for (int i = 0; i < SC; ++i) {
         mbar_init(&bar_s[i], 32);
-        mbar_init(&bar_sfree[i], 4);
+        mbar_init(&bar_sfree[i], 4 * G);
       }
       for (int i = 0; i < 4; ++i) {
-        mbar_init(&bar_recv[i], cluster);
-        mbar_init(&bar_rfree[i], cluster);
+        mbar_init(&bar_recv[i], cluster * G);
+        mbar_init(&bar_rfree[i], cluster * G);
       }
       mbar_init(&bar_drain, 1);
       abort_sh = 0;
@@ -405,57 +408,64 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp >= 4) {
-    const int q = warp & 3, r = q * 32 + lane;
+    const int q = warp & 3, r = q * 32 + lane, grp = G > 1 ? (warp - 4) >> 2 : 0;
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
     int p = 0, sp = 0;
     uint32_t pph = 0, sph = 0, uph = 0;
     bool ok = true;
     pdl_wait();  // y
-    constexpr int CW = BN < 32 ? BN : 32;  // columns per load
-    constexpr int NC = BN / CW;
+    constexpr int NC = BN / 16 / G;  // pieces of 16 columns: piece i is columns 16 (i G + grp) ..
     for (Walk<BN, GROUPED> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
       const int n_out = w.tile * kFp8Block + r;
       const float bias = a.out.bias && n_out < a.N ? __ldg(a.out.bias + (size_t)w.e * a.N + n_out) : 0.f;
-      float acc[BN];
+      float acc[NC][16];
 #pragma unroll
-      for (int c = 0; c < BN; ++c) acc[c] = 0.f;
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[i][j] = 0.f;
+      auto live = [&](int i) { return 16 * (i * G + grp) < w.ntok; };
       for (int kb = kb0; kb < kb1; kb += KP) {
         const int nk = min(KP, kb1 - kb);
         if (!(ok = wait_bar_warp(lane & 1 ? &bar_p[p] : &bar_s[sp], lane & 1 ? pph : sph, abrt))) break;
         tc_fence_after();
-        // P in pieces of CW columns, the next piece loading while this one is added
-        uint32_t d[2][CW];
-        auto live = [&](int i) { return i / NC < nk && i % NC * CW < w.ntok; };
-        auto load = [&](int i) {
-          const uint32_t at = lane_base + (p * KP + i / NC) * BN + i % NC * CW;
-          tmem_ld16(at, *reinterpret_cast<uint32_t(*)[16]>(d[i & 1]));
-          if (CW > 16) tmem_ld16(at + 16, *reinterpret_cast<uint32_t(*)[16]>(d[i & 1] + CW - 16));
+        // the next block's P loads while this one's is added
+        uint32_t d[2][NC][16];
+        auto load = [&](int k) {
+#pragma unroll
+          for (int i = 0; i < NC; ++i)
+            if (live(i)) tmem_ld16(lane_base + (p * KP + k) * BN + 16 * (i * G + grp), d[k & 1][i]);
         };
         load(0);
 #pragma unroll
-        for (int i = 0; i < KP * NC; ++i) {
-          if (live(i)) tmem_wait_ld();
-          if (i + 1 < KP * NC && live(i + 1)) load(i + 1);
-          if (!live(i)) continue;
-          const float* s = sc[sp][i / NC];
-          const float ws = s[BN];
-          const int c0 = i % NC * CW;
+        for (int k = 0; k < KP; ++k) {
+          if (k < nk) {
+            tmem_wait_ld();
+            if (k + 1 < nk) {
+              load(k + 1);
+            } else {  // all of the stage has been read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bar_pfree[p]);
+            }
+            const float* s = sc[sp][k];
+            const float ws = s[BN];
 #pragma unroll
-          for (int j = 0; j < CW; j += 4) {
-            const float4 s4 = *reinterpret_cast<const float4*>(s + c0 + j);
-            const uint32_t(&v)[CW] = d[i & 1];
-            acc[c0 + j] = fmaf(__uint_as_float(v[j]) * s4.x, ws, acc[c0 + j]);
-            acc[c0 + j + 1] = fmaf(__uint_as_float(v[j + 1]) * s4.y, ws, acc[c0 + j + 1]);
-            acc[c0 + j + 2] = fmaf(__uint_as_float(v[j + 2]) * s4.z, ws, acc[c0 + j + 2]);
-            acc[c0 + j + 3] = fmaf(__uint_as_float(v[j + 3]) * s4.w, ws, acc[c0 + j + 3]);
+            for (int i = 0; i < NC; ++i)
+              if (live(i)) {
+                const uint32_t(&v)[16] = d[k & 1][i];
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 s4 = *reinterpret_cast<const float4*>(s + 16 * (i * G + grp) + j);
+                  acc[i][j] = fmaf(__uint_as_float(v[j]) * s4.x, ws, acc[i][j]);
+                  acc[i][j + 1] = fmaf(__uint_as_float(v[j + 1]) * s4.y, ws, acc[i][j + 1]);
+                  acc[i][j + 2] = fmaf(__uint_as_float(v[j + 2]) * s4.z, ws, acc[i][j + 2]);
+                  acc[i][j + 3] = fmaf(__uint_as_float(v[j + 3]) * s4.w, ws, acc[i][j + 3]);
+                }
+              }
           }
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&bar_pfree[p]);
-          mbar_arrive(&bar_sfree[sp]);
-        }
+        if (lane == 0) mbar_arrive(&bar_sfree[sp]);
         if (++p == S) p = 0, pph ^= 1;
         if (++sp == SC) sp = 0, sph ^= 1;
       }
@@ -463,8 +473,12 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
       if (cluster == 1) {
         if (n_out < a.N) {
 #pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (c < w.ntok) put_out(a.out, (size_t)(w.row + c) * a.N + n_out, acc[c] + bias);
+          for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int c = 16 * (i * G + grp) + j;
+              if (c < w.ntok) put_out(a.out, (size_t)(w.row + c) * a.N + n_out, acc[i][j] + bias);
+            }
         }
         continue;
       }
@@ -472,17 +486,21 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
       if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(&bar_rfree[q], uph ^ 1, abrt)))) break;
       const uint32_t mine = smem_u32(recv) + (uint32_t)(rank * own * kFp8Block + r) * 4u;
 #pragma unroll
-      for (int c = 0; c < BN; ++c)
-        if (c < w.ntok) {
-          const int dst = (c * own_inv) >> 16;
-          st_cluster_f32(map_to_rank(mine + (uint32_t)((c - dst * own) * kFp8Block) * 4u, dst), acc[c]);
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int c = 16 * (i * G + grp) + j;
+          if (c < w.ntok) {
+            const int dst = (c * own_inv) >> 16;
+            st_cluster_f32(map_to_rank(mine + (uint32_t)((c - dst * own) * kFp8Block) * 4u, dst), acc[i][j]);
+          }
         }
       __syncwarp();
       if (lane < cluster) mbar_arrive_rank(&bar_recv[q], lane);
       if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(&bar_recv[q], uph, abrt)))) break;
       const int mine_n = min(own, w.ntok - rank * own);
-#pragma unroll 4
-      for (int c = 0; c < mine_n; ++c) {
+#pragma unroll 2
+      for (int c = grp; c < mine_n; c += G) {
         float v = 0.f;
 #pragma unroll 4
         for (int s = 0; s < cluster; ++s) v += recv[(s * own + c) * kFp8Block + r];
@@ -517,7 +535,7 @@ struct ClusterFit {
   int device;
   int fit[17];
 };
-cudaError_t cluster_fit(const void* kern, int device, size_t smem, const int** fit) {
+cudaError_t cluster_fit(const void* kern, int device, int threads, size_t smem, const int** fit) {
   static std::mutex mu;
   static std::vector<std::unique_ptr<ClusterFit>> known;
   std::lock_guard<std::mutex> lock(mu);
@@ -534,7 +552,7 @@ cudaError_t cluster_fit(const void* kern, int device, size_t smem, const int** f
   for (int c = 1; c <= 16; ++c) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c);
-    cfg.blockDim = dim3(kSkThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -558,37 +576,61 @@ cudaError_t cluster_fit(const void* kern, int device, size_t smem, const int** f
 
 cudaError_t fp8_out_map(CUtensorMap* tm, const Fp8Out& out, uint64_t N, uint64_t M);
 
+// Blocks of `tokens` rows that the experts have, exact for one expert. For
+// several the host knows only M: about min(experts, M) of them have rows, and
+// the last block of each is half full.
+template <bool GROUPED>
+int64_t token_blocks(const MmArgs& a, int tokens) {
+  if (!GROUPED || a.n_experts == 1) return (a.M + tokens - 1) / tokens;
+  const int64_t used = std::min(a.n_experts, a.M);
+  return std::max<int64_t>(used, (a.M + used * tokens / 2) / tokens);
+}
+
+// How a call runs: the cluster size and the microseconds it may take. The
+// model is a kernel's start and end, and for each round of units the blocks of
+// K that one CTA works through, fitted to measurements of N x K = 2048 x 2048,
+// 11008 x 2048, 3584 x 14336 and of 8 and 64 experts at M = 8 .. 12288, which
+// it meets within some 20 %; it only has to rank the kernels.
+struct Plan {
+  int cluster;
+  double us;
+};
 template <int BN, bool GROUPED>
-cudaError_t launch_skinny(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cudaStream_t s) {
+cudaError_t plan_skinny(const hxq_fp8& h, const MmArgs& a, Plan* plan, const int** fit) {
+  cudaError_t e = cluster_fit(reinterpret_cast<const void*>(fp8_skinny_kernel<BN, GROUPED>), h.device, Sk<BN>::kThreads,
+                              Sk<BN>::smem(GROUPED ? kFp8MaxExperts : 0), fit);
+  if (e != cudaSuccess) return e;
+  constexpr double kBlock = BN == 16 ? 0.2 : BN == 32 ? 0.26 : 0.43, kExchange = BN <= 32 ? 0.9 : 1.3;
+  const int64_t units = a.n_tiles * token_blocks<GROUPED>(a, BN);
+  *plan = {1, 1e30};
+  for (int c = 1; c <= Sk<BN>::kMaxCluster && c <= a.n_blocks; ++c) {
+    if ((*fit)[c] < 1) continue;
+    // (the units of several experts are a guess: a third of a round's loss on average)
+    const double rounds = GROUPED && a.n_experts > 1 ? std::max(1.0, (double)units / (*fit)[c] + 0.3)
+                                                     : (double)((units + (*fit)[c] - 1) / (*fit)[c]);
+    const double us = 4.0 + rounds * ((a.n_blocks + c - 1) / c) * kBlock + (c > 1 ? 1.0 + kExchange * rounds : 0.0);
+    if (us < plan->us) *plan = {c, us};
+    if (units * c > 2 * h.num_sms) break;  // larger clusters only add rounds
+  }
+  return cudaSuccess;
+}
+
+template <int BN, bool GROUPED>
+cudaError_t launch_skinny(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, const Plan& plan, const int* fit,
+                          cudaStream_t s) {
   CUtensorMap tmx;
-  cudaError_t e = fp8_tensor_map(&tmx, xq, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)fp8_ld(a.K), BN);
+  const cudaError_t e = fp8_tensor_map(&tmx, xq, (uint64_t)a.K, (uint64_t)a.M, (uint64_t)fp8_ld(a.K), BN);
   if (e != cudaSuccess) return e;
   auto kern = fp8_skinny_kernel<BN, GROUPED>;
   const size_t smem = Sk<BN>::smem(GROUPED ? a.n_experts : 0);
-  const int* fit = nullptr;
-  if ((e = cluster_fit(reinterpret_cast<const void*>(kern), h.device, Sk<BN>::smem(GROUPED ? kFp8MaxExperts : 0), &fit)) !=
-      cudaSuccess)
-    return e;
-  // units: exact for one layer; experts with rows have at most one block of
-  // tokens that is not full, and about min(experts, rows) have rows
-  const int used = std::min(a.n_experts, a.M);
-  const int64_t most = (int64_t)a.n_tiles * (GROUPED ? used + a.M / BN : (a.M + BN - 1) / BN);
-  const int64_t likely = (int64_t)a.n_tiles * std::max<int64_t>(GROUPED ? used : 0, (a.M + BN - 1) / BN);
-  // CTAs per unit: the blocks of K that the busiest cluster's CTAs work
-  // through one after another, plus what a unit's exchange costs
-  int c = 1;
-  int64_t best = INT64_MAX;
-  for (int t = 1; t <= Sk<BN>::kMaxCluster && t <= a.n_blocks; ++t) {
-    if (fit[t] < 1) continue;
-    const int64_t rounds = (likely + fit[t] - 1) / fit[t];
-    const int64_t cost = rounds * ((a.n_blocks + t - 1) / t + (t > 1 ? 2 : 0)) + (t > 1 ? 6 : 0);
-    if (cost < best) best = cost, c = t;
-  }
-  const int own = (BN + c - 1) / c;
-  const int own_inv = (65536 + own - 1) / own;  // (c * own_inv) >> 16 = c / own for c < BN
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(most, fit[c])) * c;
-  if (c == 1) return launch_pdl(kern, (unsigned)grid, kSkThreads, smem, s, h.tm_w, tmx, a, c, own, own_inv);
-  return launch_pdl_cluster(kern, (unsigned)grid, kSkThreads, smem, (unsigned)c, s, h.tm_w, tmx, a, c, own, own_inv);
+  // no more clusters than there can be units
+  const int64_t most =
+      (int64_t)a.n_tiles * (GROUPED ? std::min(a.n_experts, a.M) + a.M / BN : (a.M + BN - 1) / BN);
+  const int c = plan.cluster, own = (BN + c - 1) / c;
+  const int own_inv = (65536 + own - 1) / own;  // (x * own_inv) >> 16 = x / own for x < BN
+  const unsigned grid = (unsigned)(std::min<int64_t>(most, fit[c]) * c);
+  if (c == 1) return launch_pdl(kern, grid, Sk<BN>::kThreads, smem, s, h.tm_w, tmx, a, c, own, own_inv);
+  return launch_pdl_cluster(kern, grid, Sk<BN>::kThreads, smem, (unsigned)c, s, h.tm_w, tmx, a, c, own, own_inv);
 }
 
 // ---- many tokens ----------------------------------------------------------------
@@ -1042,14 +1084,29 @@ cudaError_t launch_wide(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cu
 }
 
 template <bool GROUPED>
+double wide_us(const hxq_fp8& h, const MmArgs& a) {
+  const int64_t units = (a.n_tiles + 1) / 2 * token_blocks<GROUPED>(a, kWideTokens), pairs = h.num_sms / 2;
+  const int64_t rest = units % pairs;  // cut as the kernel cuts them
+  const double last = rest == 0 ? 0.0 : rest * 4 <= pairs ? 0.355 : rest * 2 <= pairs ? 0.43 : 0.55;
+  return 5.0 + (units / pairs * 0.55 + last) * a.n_blocks;
+}
+
+template <bool GROUPED>
 cudaError_t launch_mm(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, cudaStream_t s) {
-  // tokens an expert gets on average decide the block of tokens
-  const int per = GROUPED ? (a.M + a.n_experts - 1) / a.n_experts : a.M;
-  if (per <= 16) return launch_skinny<16, GROUPED>(h, xq, a, s);
-  if (per <= 32) return launch_skinny<32, GROUPED>(h, xq, a, s);
-  if (per <= 64) return launch_skinny<64, GROUPED>(h, xq, a, s);
-  if (per <= 128) return launch_skinny<128, GROUPED>(h, xq, a, s);
-  return launch_wide<GROUPED>(h, xq, a, s);
+  Plan p16, p32, p64;
+  const int *f16, *f32, *f64;
+  cudaError_t e = plan_skinny<16, GROUPED>(h, a, &p16, &f16);
+  if (e != cudaSuccess) return e;
+  // up to 16 rows in all, wider blocks only add work
+  if (a.M <= 16) return launch_skinny<16, GROUPED>(h, xq, a, p16, f16, s);
+  if ((e = plan_skinny<32, GROUPED>(h, a, &p32, &f32)) != cudaSuccess ||
+      (e = plan_skinny<64, GROUPED>(h, a, &p64, &f64)) != cudaSuccess)
+    return e;
+  const double best = std::min({p16.us, p32.us, p64.us});
+  if (wide_us<GROUPED>(h, a) <= best) return launch_wide<GROUPED>(h, xq, a, s);
+  if (p16.us <= best) return launch_skinny<16, GROUPED>(h, xq, a, p16, f16, s);
+  if (p32.us <= best) return launch_skinny<32, GROUPED>(h, xq, a, p32, f32, s);
+  return launch_skinny<64, GROUPED>(h, xq, a, p64, f64, s);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

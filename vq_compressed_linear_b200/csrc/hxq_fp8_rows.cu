@@ -17,6 +17,9 @@
 
 #include <algorithm>
 #include <climits>
+#include <mutex>
+#include <new>
+#include <vector>
 
 #include "hxq_fp8.cuh"
 
@@ -91,14 +94,21 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int n, const floa
 
 __device__ __forceinline__ float round_bf16(float f) { return __bfloat162float(__float2bfloat16_rn(f)); }
 
-// e4m3 bytes of 4 values already divided by their scale. Infinities become
-// NaN (e4m3 has none), like NaN: 0 * v adds NaN exactly then.
+// e4m3 bytes of 4 values already divided by their scale (NaN gives NaN; an
+// infinity would give 448: see no_infinities).
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
-  const __nv_fp8x2_storage_t lo =
-      __nv_cvt_float2_to_fp8x2(make_float2(fmaf(a, 0.f, a), fmaf(b, 0.f, b)), __NV_SATFINITE, __NV_E4M3);
-  const __nv_fp8x2_storage_t hi =
-      __nv_cvt_float2_to_fp8x2(make_float2(fmaf(c, 0.f, c), fmaf(d, 0.f, d)), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+// Infinities become NaN (e4m3 has none) in a block whose maximum is infinite:
+// 0 * v adds NaN to them and nothing to the others.
+template <int N>
+__device__ __forceinline__ void no_infinities(float (&v)[N], float amax) {
+  if (isinf(amax)) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = fmaf(v[j], 0.f, v[j]);
+  }
 }
 
 __device__ __forceinline__ float absmax8(const float (&v)[8]) {
@@ -129,81 +139,326 @@ __device__ __forceinline__ void put8(uint8_t* row, int64_t ld, int c, const floa
   *reinterpret_cast<uint2*>(row + c) = w;
 }
 
-// silu(g) * u. The fp32 form is off by a few 2^-24 relative: one rounding
-// each in the exponential (2 ulp), the sum, the quotient and the product.
-__device__ __forceinline__ float swiglu(float g, float u) { return g / (1.f + expf(-g)) * u; }
-__device__ __forceinline__ double swiglu64(float g, float u) { return (double)g / (1.0 + exp(-(double)g)) * (double)u; }
+// silu(g) * u = u g / (1 + e^-g). e^-g = 2^p (1 + r ln 2) with p = -g log2(e)
+// rounded and r what the rounding left (exact by FMA, plus the constant's own
+// tail): 2^p is the hardware's (2 ulp), the reciprocal too (1 ulp), and four
+// more roundings follow. g is taken as -87 below that, where e^-g nears the
+// end of fp32: the value is then below 1e-35 u, 0 beside any block maximum
+// that is not formed again in 64 bits.
+__device__ __forceinline__ float swiglu(float g, float u) {
+  constexpr float kLog2e = 1.44269504f;                            // log2(e) to fp32,
+  constexpr float kLog2eTail = (float)(1.4426950408889634 - 1.44269504f);  // and the rest
+  const float x = -fmaxf(g, -87.f);
+  const float p = x * kLog2e;
+  const float r = fmaf(x, kLog2eTail, fmaf(x, kLog2e, -p));
+  float e, inv;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p));
+  e = fmaf(e * r, 0.693147181f, e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(1.f + e));
+  return g * inv * u;
+}
+// One lane's part of a block formed in 64 bits, for blocks whose scale fp32
+// cannot settle (a call: its registers are not the fast path's).
+template <bool BF16, bool VEC>
+__device__ __noinline__ void swiglu64(const void* x, int64_t at, int cols, int n, uint8_t* row, int64_t ld, int c,
+                                      float* scale) {
+  float g[8], v[8];
+  load8<BF16, VEC>(x, at, n, g);
+  load8<BF16, VEC>(x, at + cols, n, v);
+  double m = 0.0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const double d = (double)g[j] / (1.0 + exp(-(double)g[j])) * (double)v[j];
+    m = fmax(m, fabs(d));
+    v[j] = (float)d;
+  }
+  m = block_max(m);
+  float inv;
+  const float s = fp8_scale(m, &inv);
+  no_infinities(v, (float)m);
+  if (row) put8(row, ld, c, v, inv);
+  if (scale) *scale = s;
+}
 
-// One half-warp per block of 128, blocks numbered row-major; GATED: x is
-// gate|up of 2 * cols columns.
-template <bool BF16, bool VEC, bool GATED>
-__global__ void __launch_bounds__(256) quantize_kernel(const void* __restrict__ x, uint32_t n_all, int cols, int kb,
-                                                      int64_t ld, uint8_t* __restrict__ q,
+// n / d for n < 2^31: with l = ceil(log2 d), m = floor(2^(31 + l) / d) + 1 the
+// quotient is n m >> (31 + l) (Granlund and Montgomery's round-up method).
+struct FastDiv {
+  uint32_t m, s, d;
+};
+FastDiv fast_div(uint32_t d) {
+  uint32_t l = 0;
+  while (((uint64_t)1 << l) < d) ++l;
+  return {(uint32_t)((((uint64_t)1 << (31 + l)) / d) + 1), l, d};
+}
+__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
+  return f.s ? __umulhi(n, f.m) >> (f.s - 1) : n;
+}
+
+// One half-warp per block of 128, blocks numbered row-major, U of them per
+// half-warp (16 U CTA-wide apart), all loaded before the first is worked on:
+// with one, a thread has 16 bytes of bf16 in flight. GATED: x is gate|up of
+// 2 * cols columns.
+template <bool BF16, bool VEC, bool GATED, int U>
+__global__ void __launch_bounds__(256) quantize_kernel(const void* __restrict__ x, uint32_t n_all, int cols,
+                                                      FastDiv kb, int64_t ld, uint8_t* __restrict__ q,
                                                       float* __restrict__ scales) {
   pdl_launch_dependents();
   pdl_wait();
   const int sub = threadIdx.x & (kLanesPerBlock - 1);
-  // whole warps take part in the shuffles: a warp covers two blocks, the second may be past the end
-  const uint32_t step = gridDim.x * (blockDim.x / kLanesPerBlock);
-  for (uint32_t i0 = blockIdx.x * (blockDim.x / kLanesPerBlock) + (threadIdx.x / 32) * 2; i0 < n_all; i0 += step) {
-    const uint32_t i = i0 + ((threadIdx.x >> 4) & 1);
-    const bool live = i < n_all;
-    const int64_t row = live ? i / (uint32_t)kb : 0;
-    const int b = live ? (int)(i - (uint32_t)row * kb) : 0;
-    const int c = b * kFp8Block + sub * kVec;
-    const int n = live ? cols - c : 0;
-    float v[8];
+  // whole warps take part in the shuffles: a block past the end has no columns
+  const uint32_t i0 = blockIdx.x * (16 * U) + threadIdx.x / kLanesPerBlock;
+  float v[U][8], g[GATED ? U : 1][8];
+  uint32_t row[U];
+  int c[U];
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const uint32_t i = i0 + k * 16;
+    row[k] = div_by(i, kb);
+    c[k] = (int)(i - row[k] * kb.d) * kFp8Block + sub * kVec;
+    const int n = i < n_all ? cols - c[k] : 0;
     if (GATED) {
-      float g[8], u[8];
-      load8<BF16, VEC>(x, row * 2 * cols + c, n, g);
-      load8<BF16, VEC>(x, row * 2 * cols + cols + c, n, u);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = swiglu(g[j], u[j]);
-      float inv, amax = block_max(absmax8(v));
-      float s = fp8_scale(amax, &inv);
-      if (__any_sync(0xffffffffu, live && fp8_scale_unsure(amax))) {
-        double m = 0.0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const double d = swiglu64(g[j], u[j]);
-          m = fmax(m, fabs(d));
-          v[j] = (float)d;
-        }
-        s = fp8_scale(block_max(m), &inv);
-      }
-      if (live) {
-        put8(q + row * ld, ld, c, v, inv);
-        if (sub == 0) scales[i] = s;
-      }
+      load8<BF16, VEC>(x, (int64_t)row[k] * 2 * cols + c[k], n, g[k]);
+      load8<BF16, VEC>(x, (int64_t)row[k] * 2 * cols + cols + c[k], n, v[k]);
     } else {
-      load8<BF16, VEC>(x, row * cols + c, n, v);
-      float inv;
-      const float s = fp8_scale(block_max(absmax8(v)), &inv);
-      if (live) {
-        put8(q + row * ld, ld, c, v, inv);
-        if (sub == 0) scales[i] = s;
-      }
+      load8<BF16, VEC>(x, (int64_t)row[k] * cols + c[k], n, v[k]);
     }
+  }
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const uint32_t i = i0 + k * 16;
+    float inv;
+    if (GATED) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[k][j] = swiglu(g[k][j], v[k][j]);
+    }
+    const float amax = block_max(absmax8(v[k]));
+    const float s = fp8_scale(amax, &inv);
+    uint8_t* out = i < n_all ? q + row[k] * ld : nullptr;
+    float* to = i < n_all && sub == 0 ? scales + i : nullptr;
+    if (GATED && __any_sync(0xffffffffu, i < n_all && fp8_scale_unsure(amax))) {
+      swiglu64<BF16, VEC>(x, (int64_t)row[k] * 2 * cols + c[k], cols, i < n_all ? cols - c[k] : 0, out, ld, c[k], to);
+      continue;
+    }
+    no_infinities(v[k], amax);
+    if (out) put8(out, ld, c[k], v[k], inv);
+    if (to) *to = s;
   }
 }
 
-// One CTA per row. Thread t holds the columns 8 (i T + t) .. + 7, i < NCH, in
-// registers between the sum of squares and the output; NCH = 0: rows longer
-// than the registers hold, read twice.
-template <bool XBF16, bool RBF16, bool VEC, int NCH>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
+// A thread's 8 elements as they lie in shared memory (bf16: 16 bytes, fp32: 32).
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const uint8_t* p, float (&v)[8]) {
+  uint32_t u[BF16 ? 4 : 8];
+#pragma unroll
+  for (int k = 0; k < (BF16 ? 1 : 2); ++k) {
+    const uint4 w = reinterpret_cast<const uint4*>(p)[k];
+    u[4 * k] = w.x; u[4 * k + 1] = w.y; u[4 * k + 2] = w.z; u[4 * k + 3] = w.w;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = __uint_as_float(!BF16 ? u[j] : j & 1 ? u[j / 2] & 0xFFFF0000u : u[j / 2] << 16);
+}
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// What both norm kernels do with a thread's 8 values t of one chunk (columns
+// c ..), their weights and the row's statistics: h = t rstd g as bf16 and / or
+// 8 bits. mean64(): the mean of squares (plus eps) in 64 bits, asked for by a
+// whole warp and only where it decides a scale.
+template <bool VEC, typename Mean64>
+__device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t ld, int kb, int c,
+                                         const float (&t)[8], const float (&g)[8], float rstd, Mean64 mean64) {
+  const int n = a.cols - c;
+  float h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) h[j] = t[j] * rstd * g[j];
+  if (a.q) {
+    float inv;
+    const float amax = block_max(absmax8(h));
+    float s = fp8_scale(amax, &inv);
+    bool unsure = c - (int)(threadIdx.x & (kLanesPerBlock - 1)) * kVec < a.cols && fp8_scale_unsure(amax);
+    if (__any_sync(0xffffffffu, unsure)) {
+      if (amax < 1e-30f) {  // tiny, or a block of zeros: nothing is unsure about that
+        float any = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) any = fmaxf(any, t[j] != 0.f && g[j] != 0.f ? 1.f : 0.f);
+        unsure = unsure && any != 0.f;
+      }
+      if (__any_sync(0xffffffffu, unsure)) {
+        const double r = 1.0 / sqrt(mean64());
+        double m = 0.0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const double e = (double)t[j] * r * (double)g[j];
+          m = fmax(m, fabs(e));
+          h[j] = (float)e;
+        }
+        s = fp8_scale(block_max(m), &inv);
+      }
+    }
+    if (a.y) store8<true, VEC>(a.y, row * a.cols + c, n, h);
+    no_infinities(h, amax);
+    put8(a.q + row * ld, ld, c, h, inv);
+    const int b = c / kFp8Block;
+    if ((threadIdx.x & (kLanesPerBlock - 1)) == 0 && b < kb) a.scales[row * kb + b] = s;
+  } else {
+    store8<true, VEC>(a.y, row * a.cols + c, n, h);
+  }
+}
+// 1 / sqrt of a mean of squares that may lie beyond the range of fp32.
+__device__ __forceinline__ float root(float mean) { return rsqrtf(mean); }
+__device__ __forceinline__ float root(double mean) {
+  return mean > 1e37 || mean < 1e-37 ? (float)(1.0 / sqrt(mean)) : rsqrtf((float)mean);
+}
+
+// Rows blockIdx.x, + gridDim.x, ... one after another; thread t has the columns
+// 8 (i T + t) .. + 7 for i < NCH, and their weights in registers. It copies its
+// own pieces of the next rows into shared memory (cp.async, D slots): a slot
+// is filled again after the next row's barrier, when no warp can still want
+// the row for its mean in 64 bits.
+// The kernel is bound by issue slots (48 instructions an element, most of them
+// per row and thread, made 8192 x 3584 take 56 us): so two chunks a thread,
+// sums in fp32 (17 roundings deep at most), and 64 bits only on demand.
+template <bool XBF16, bool RBF16, int NCH, int D>
+__global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs a, int64_t rows) {
+  constexpr int XB = XBF16 ? 16 : 32, RB = RBF16 ? 16 : 32;  // bytes of 8 elements
+  const int T = blockDim.x, tid = threadIdx.x, cols = a.cols;
+  const int64_t ld = fp8_ld(cols), step = gridDim.x;
+  const int kb = fp8_blocks(cols);
+  extern __shared__ __align__(16) uint8_t ring[];  // [D][NCH][T] pieces of x, then of the residual
+  __shared__ float part[2][32];
+  pdl_launch_dependents();
+  auto col = [&](int i) { return (i * T + tid) * kVec; };
+  auto xslot = [&](int d, int i, int t) { return ring + ((d * NCH + i) * T + t) * XB; };
+  auto rslot = [&](int d, int i, int t) { return ring + D * NCH * T * XB + ((d * NCH + i) * T + t) * RB; };
+  const uint8_t* px = static_cast<const uint8_t*>(a.x) + ((int64_t)blockIdx.x * cols + tid * kVec) * (XB / 8);
+  const uint8_t* pr = static_cast<const uint8_t*>(a.res) + ((int64_t)blockIdx.x * cols + tid * kVec) * (RB / 8);
+  const int64_t xstep = step * cols * (XB / 8), rstep = step * cols * (RB / 8);
+  int64_t fetched = blockIdx.x;
+  auto fetch = [&](int d) {  // the next row into slot d
+    if (fetched < rows) {
+#pragma unroll
+      for (int i = 0; i < NCH; ++i)
+        if (col(i) < cols) {
+          cp_async16(xslot(d, i, tid), px + i * T * XB);
+          if (!XBF16) cp_async16(xslot(d, i, tid) + 16, px + i * T * XB + 16);
+          if (a.res) {
+            cp_async16(rslot(d, i, tid), pr + i * T * RB);
+            if (!RBF16) cp_async16(rslot(d, i, tid) + 16, pr + i * T * RB + 16);
+          }
+        }
+    }
+    fetched += step;
+    px += xstep;
+    pr += rstep;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // t = x + res, rounded to the residual's type: what the next layer's
+  // residual holds and what the norm of the unfused sequence would read; the
+  // 16 bytes of a bf16 t come along as they are stored
+  auto load_t = [&](int d, int i, int t, float (&v)[8], uint4& w) {
+    unpack8<XBF16>(xslot(d, i, t), v);
+    if (a.res) {
+      float r[8];
+      unpack8<RBF16>(rslot(d, i, t), r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += r[j];
+      if (RBF16) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+          u[j] = *reinterpret_cast<const uint32_t*>(&p);
+          v[2 * j] = __uint_as_float(u[j] << 16);
+          v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+        }
+        w = make_uint4(u[0], u[1], u[2], u[3]);
+      }
+    }
+  };
+  pdl_wait();
+#pragma unroll
+  for (int d = 0; d < (D > 1 ? D - 1 : 1); ++d) fetch(d);
+  float g[NCH][8];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    if (a.weight) {
+      load8<false, true>(a.weight, col(i), cols - col(i), g[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[i][j] = 1.f;
+    }
+  }
+  const float inv_cols = 1.f / (float)cols;
+  int flip = 0, d = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += step, flip ^= 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(D > 1 ? D - 2 : 0) : "memory");  // the oldest row
+    float t[NCH][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      if (col(i) < cols) {
+        uint4 w;
+        load_t(d, i, tid, t[i], w);
+        if (a.sum) {
+          if (RBF16)
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.sum) + row * cols + col(i)) = w;
+          else
+            store8<false, true>(a.sum, row * cols + col(i), 8, t[i]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[i][j] = 0.f;
+      }
+      float q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = fmaf(t[i][j + 4], t[i][j + 4], t[i][j] * t[i][j]);
+      ss += (q[0] + q[1]) + (q[2] + q[3]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if ((tid & 31) == 0) part[flip][tid >> 5] = ss;
+    __syncthreads();  // (the other half of `part` is written before the next barrier)
+    if (D > 1) fetch(d == 0 ? D - 1 : d - 1);  // the last row's slot
+    ss = (tid & 31) < T / 32 ? part[flip][tid & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // the row's mean of squares in 64 bits, by one warp from shared memory
+    auto mean64 = [&]() {
+      double s64 = 0.0;
+      for (int k = tid & 31; k < (cols + kVec - 1) / kVec; k += 32) {
+        float v[8];
+        uint4 w;
+        load_t(d, k / T, k % T, v, w);
+        for (int j = 0; j < 8; ++j) s64 = fma((double)v[j], (double)v[j], s64);
+      }
+      for (int o = 16; o; o >>= 1) s64 += __shfl_xor_sync(0xffffffffu, s64, o);
+      return s64 / cols + (double)a.eps;
+    };
+    const float mean = fmaf(ss, inv_cols, a.eps);
+    float rstd = root(mean);
+    if (!(mean < 1e37f && mean > 1e-30f)) rstd = root(mean64());  // squares beyond the range of fp32
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) norm_out<true>(a, row, ld, kb, col(i), t[i], g[i], rstd, mean64);
+    if (D == 1) {
+      __syncthreads();  // every warp is done with the slot
+      fetch(0);
+    }
+    d = d + 1 == D ? 0 : d + 1;
+  }
+}
+
+// Rows longer than that, or not of whole 16-byte pieces: one CTA per row, the
+// row read twice, the sum in 64 bits.
+template <bool XBF16, bool RBF16, bool VEC>
+__global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
   const int64_t row = blockIdx.x;
   const int T = blockDim.x, tid = threadIdx.x, cols = a.cols;
-  const int64_t ld = fp8_ld(cols);
-  const int kb = fp8_blocks(cols), n_ch = (cols + kVec - 1) / kVec;
-  const int iters = NCH ? NCH : (n_ch + T - 1) / T;
+  const int iters = ((cols + kVec - 1) / kVec + T - 1) / T;
   __shared__ double part[32];
   pdl_launch_dependents();
   pdl_wait();
-  float t[NCH ? NCH : 1][8];
-
-  // t = x + res, rounded to the residual's type: what the next layer's
-  // residual holds and what the norm of the unfused sequence would read
   auto load_t = [&](int i, float (&v)[8]) {
     const int c = (i * T + tid) * kVec;
     load8<XBF16, VEC>(a.x, row * cols + c, cols - c, v);
@@ -214,71 +469,33 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
       for (int j = 0; j < 8; ++j) v[j] = RBF16 ? round_bf16(v[j] + r[j]) : v[j] + r[j];
     }
   };
-  // the sum of squares in 64 bits: the scales follow from it
   double ss = 0.0;
-  if (NCH) {
+  float t[8];
+  for (int i = 0; i < iters; ++i) {
+    load_t(i, t);
 #pragma unroll
-    for (int i = 0; i < (NCH ? NCH : 1); ++i) load_t(i, t[i]);
-#pragma unroll
-    for (int i = 0; i < (NCH ? NCH : 1); ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fma((double)t[i][j], (double)t[i][j], ss);
-  } else {
-    for (int i = 0; i < iters; ++i) {
-      load_t(i, t[0]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fma((double)t[0][j], (double)t[0][j], ss);
-    }
+    for (int j = 0; j < 8; ++j) ss = fma((double)t[j], (double)t[j], ss);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if ((tid & 31) == 0) part[tid >> 5] = ss;
   __syncthreads();
-  ss = (tid & 31) < T / 32 ? part[tid & 31] : 0.0;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  ss = 0.0;
+  for (int w = 0; w < T / 32; ++w) ss += part[w];
   const double mean = ss / cols + (double)a.eps;
-  // (sums of squares beyond the range of fp32: the root in 64 bits)
-  const float rstd = mean > 1e37 || mean < 1e-37 ? (float)(1.0 / sqrt(mean)) : rsqrtf((float)mean);
-
+  const float rstd = root(mean);
+  for (int i = 0; i < iters; ++i) {
+    const int c = (i * T + tid) * kVec;
+    load_t(i, t);
+    if (a.sum) store8<RBF16, VEC>(a.sum, row * cols + c, cols - c, t);
+    float g[8];
+    if (a.weight) {
+      load8<false, VEC>(a.weight, c, cols - c, g);
+    } else {
 #pragma unroll
-  for (int i = 0; i < (NCH ? NCH : 1); ++i) {
-    for (int ii = i; ii < (NCH ? i + 1 : iters); ++ii) {
-      if (!NCH) load_t(ii, t[0]);
-      const int c = (ii * T + tid) * kVec, n = cols - c;
-      float (&tv)[8] = t[NCH ? i : 0];
-      if (a.sum) store8<RBF16, VEC>(a.sum, row * cols + c, n, tv);
-      float g[8], h[8];
-      if (a.weight) {
-        load8<false, VEC>(a.weight, c, n, g);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = 1.f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = tv[j] * rstd * g[j];
-      if (a.q) {
-        float inv;
-        const float amax = block_max(absmax8(h));
-        float s = fp8_scale(amax, &inv);
-        const bool live = c - (tid & (kLanesPerBlock - 1)) * kVec < cols;  // the block has columns
-        if (__any_sync(0xffffffffu, live && fp8_scale_unsure(amax))) {
-          const double r = 1.0 / sqrt(mean);
-          double m = 0.0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const double d = (double)tv[j] * r * (double)g[j];
-            m = fmax(m, fabs(d));
-            h[j] = (float)d;
-          }
-          s = fp8_scale(block_max(m), &inv);
-        }
-        put8(a.q + row * ld, ld, c, h, inv);
-        const int b = c / kFp8Block;
-        if ((tid & (kLanesPerBlock - 1)) == 0 && b < kb) a.scales[row * kb + b] = s;
-      }
-      if (a.y) store8<true, VEC>(a.y, row * cols + c, n, h);
+      for (int j = 0; j < 8; ++j) g[j] = 1.f;
     }
+    norm_out<VEC>(a, row, fp8_ld(cols), fp8_blocks(cols), c, t, g, rstd, [&]() { return mean; });
   }
 }
 
@@ -286,7 +503,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(NormArgs a) {
 // lane l the columns 4 l .. 4 l + 3, in registers between the maximum and the
 // output.
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(256) encode_kernel(const void* __restrict__ w, int N, int K, int nb, int kb,
+__global__ void __launch_bounds__(256, 2) encode_kernel(const void* __restrict__ w, int N, int K, int nb, int kb,
                                                     uint8_t* __restrict__ q, float* __restrict__ scales) {
   pdl_launch_dependents();
   pdl_wait();
@@ -343,6 +560,8 @@ __global__ void __launch_bounds__(256) encode_kernel(const void* __restrict__ w,
   const float s = fp8_scale(m, &inv);
   if (threadIdx.x == 0) scales[blk] = s;
 #pragma unroll
+  for (int i = 0; i < 16; ++i) no_infinities(v[i], m);
+#pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int r = rb * kFp8Block + i * 8 + warp;
     if (r >= N) continue;
@@ -386,31 +605,82 @@ __global__ void __launch_bounds__(256) retile_kernel(const uint8_t* __restrict__
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+template <bool BF16, bool VEC, bool GATED>
+cudaError_t launch_quant_as(const void* x, uint32_t n, int cols, uint8_t* q, float* scales, cudaStream_t s) {
+  const FastDiv kb = fast_div((uint32_t)fp8_blocks(cols));
+  // several blocks per half-warp once that still gives every SM two CTAs
+  constexpr int U = GATED ? 2 : 4;
+  auto go = [&](auto kern, int u) {
+    return launch_pdl(kern, (n + 16 * u - 1) / (16 * u), 256, 0, s, x, n, cols, kb, fp8_ld(cols), q, scales);
+  };
+  if (n >= 300u * 16 * U) return go(quantize_kernel<BF16, VEC, GATED, U>, U);
+  return go(quantize_kernel<BF16, VEC, GATED, 1>, 1);
+}
 template <bool GATED>
 cudaError_t launch_quant(const void* x, int bf16, int64_t rows, int cols, uint8_t* q, float* scales, cudaStream_t s) {
-  const int kb = fp8_blocks(cols);
-  const uint32_t n = (uint32_t)(rows * kb);  // < 2^31, checked by the caller
-  // 16 blocks of 128 per CTA; beyond 2^20 CTAs they loop
-  const unsigned grid = std::min<uint32_t>((n + 15) / 16, 1u << 20);
+  const uint32_t n = (uint32_t)(rows * fp8_blocks(cols));  // < 2^31, checked by the caller
   const bool vec = cols % 8 == 0 && aligned16(x);
-  auto go = [&](auto kern) { return launch_pdl(kern, grid, 256, 0, s, x, n, cols, kb, fp8_ld(cols), q, scales); };
-  if (bf16) return vec ? go(quantize_kernel<true, true, GATED>) : go(quantize_kernel<true, false, GATED>);
-  return vec ? go(quantize_kernel<false, true, GATED>) : go(quantize_kernel<false, false, GATED>);
+  if (bf16)
+    return vec ? launch_quant_as<true, true, GATED>(x, n, cols, q, scales, s)
+               : launch_quant_as<true, false, GATED>(x, n, cols, q, scales, s);
+  return vec ? launch_quant_as<false, true, GATED>(x, n, cols, q, scales, s)
+             : launch_quant_as<false, false, GATED>(x, n, cols, q, scales, s);
+}
+
+// CTAs of `kern` with t threads and smem bytes of dynamic shared memory that
+// are resident on the current device at once, asked once for each.
+cudaError_t resident(const void* kern, int t, size_t smem, int64_t* ctas) {
+  struct Known {
+    int device;
+    const void* kern;
+    int t;
+    size_t smem;
+    int64_t ctas;
+  };
+  static std::mutex mu;
+  static std::vector<Known> known;
+  int dev = 0, per = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const Known& k : known)
+    if (k.device == dev && k.kern == kern && k.t == t && k.smem == smem) {
+      *ctas = k.ctas;
+      return cudaSuccess;
+    }
+  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, t, smem)) != cudaSuccess ||
+      (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+    return e;
+  *ctas = (int64_t)std::max(1, per) * sms;
+  try {
+    known.push_back({dev, kern, t, smem, *ctas});
+  } catch (const std::bad_alloc&) {  // asked again next time
+  }
+  return cudaSuccess;
 }
 
 template <bool XB, bool RB, bool VEC>
 cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t s) {
-  // chunks of 8 per row, over at most 512 threads of up to 4 chunks, then
-  // 1024 threads of 4, then rows that are read twice
+  // chunks of 8 per row: one per thread up to 256 threads, then two of up to
+  // 1024, then rows that are read twice; as many CTAs as fit at once
   const int ch = (a.cols + kVec - 1) / kVec;
-  auto go = [&](auto kern, int nch) {
-    const int t = std::min(1024, ((ch + nch - 1) / nch + 31) / 32 * 32);
-    return launch_pdl(kern, (unsigned)rows, (unsigned)t, 0, s, a);
+  auto go = [&](auto kern, int nch, int depth) -> cudaError_t {
+    const int t = ((ch + nch - 1) / nch + 31) / 32 * 32;
+    const size_t smem = (size_t)depth * nch * t * ((XB ? 16 : 32) + (a.res ? RB ? 16 : 32 : 0));
+    int64_t fit = 0;
+    cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(kern));
+    if (e == cudaSuccess) e = resident(reinterpret_cast<const void*>(kern), t, smem, &fit);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, (unsigned)std::min(rows, fit), (unsigned)t, smem, s, a, rows);
   };
-  if (ch <= 512) return go(rmsnorm_kernel<XB, RB, VEC, 1>, 1);
-  if (ch <= 1024) return go(rmsnorm_kernel<XB, RB, VEC, 2>, 2);
-  if (ch <= 4096) return go(rmsnorm_kernel<XB, RB, VEC, 4>, 4);
-  return go(rmsnorm_kernel<XB, RB, VEC, 0>, 4);
+  if constexpr (VEC) {
+    if (ch <= 256) return go(rmsnorm_kernel<XB, RB, 1, 4>, 1, 4);
+    if (ch <= 1024) return go(rmsnorm_kernel<XB, RB, 2, 3>, 2, 3);
+    // (two rows of fp32 x and residual would take 2 * 2 * 1024 * 64 bytes)
+    if (ch <= 2048) return go(rmsnorm_kernel<XB, RB, 2, XB && RB ? 2 : 1>, 2, XB && RB ? 2 : 1);
+  }
+  const int t = std::min(1024, (ch + 31) / 32 * 32);
+  return launch_pdl(rmsnorm_long_kernel<XB, RB, VEC>, (unsigned)rows, (unsigned)t, 0, s, a);
 }
 
 }  // namespace
