@@ -229,7 +229,7 @@ def test_rmsnorm(hxq, M, K, xt, rt):
     res = randn(M + K + 1, M, K, scale=5.0).to(dtype(rt))
     w = 1 + randn(M + K + 2, K, scale=0.2)
     t, h = ref_norm(x, res, w, 1e-5)
-    for xx, rr, ww in ((x, res, w), (unaligned(x), unaligned(res), unaligned(w))):
+    for xx, rr, ww in ((unaligned(x), unaligned(res), unaligned(w)), (x, res, w)):
         q, s, y, total = hxq.rmsnorm(xx, ww, 1e-5, residual=rr, want="qy")
         assert torch.equal(total, t)
         check_bytes(q, s, h, K, DELTA)

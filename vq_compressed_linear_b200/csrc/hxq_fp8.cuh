@@ -99,12 +99,12 @@ __device__ __forceinline__ float fp8_scale(double amax, float* inv) {
   return __uint_as_float((uint32_t)e << 23);
 }
 // Whether an amax computed in fp32 with a relative error of a few 2^-24 could
-// belong to the next scale (its significand is next to 1.75), or is so small
-// that its terms may have underflowed: such a block is computed again in 64
+// belong to the next scale (its significand is next to 1.75), or its terms may
+// have under- or overflowed on the way: such a block is computed again in 64
 // bits, so that a scale never depends on fp32 rounding.
+__device__ __forceinline__ bool fp8_far(float v) { return !(v >= 1e-30f && v < 1e37f); }
 __device__ __forceinline__ bool fp8_scale_unsure(float amax) {
-  const uint32_t m = __float_as_uint(amax) & 0x7FFFFFu;
-  return (m - (0x600000u - 32u)) <= 64u || amax < 1e-30f;
+  return ((__float_as_uint(amax) & 0x7FFFFFu) - (0x600000u - 32u)) <= 64u || fp8_far(amax);
 }
 
 #endif  // __CUDACC__

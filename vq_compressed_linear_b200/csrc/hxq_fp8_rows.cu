@@ -104,11 +104,9 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 // Infinities become NaN (e4m3 has none) in a block whose maximum is infinite:
 // 0 * v adds NaN to them and nothing to the others.
 template <int N>
-__device__ __forceinline__ void no_infinities(float (&v)[N], float amax) {
-  if (isinf(amax)) {
+__device__ __forceinline__ void no_infinities(float (&v)[N]) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = fmaf(v[j], 0.f, v[j]);
-  }
+  for (int j = 0; j < N; ++j) v[j] = fmaf(v[j], 0.f, v[j]);
 }
 
 __device__ __forceinline__ float absmax8(const float (&v)[8]) {
@@ -139,23 +137,27 @@ __device__ __forceinline__ void put8(uint8_t* row, int64_t ld, int c, const floa
   *reinterpret_cast<uint2*>(row + c) = w;
 }
 
-// silu(g) * u = u g / (1 + e^-g). e^-g = 2^p (1 + r ln 2) with p = -g log2(e)
+// silu(g) * u of two elements. e^-g = 2^p (1 + r ln 2) with p = -g log2(e)
 // rounded and r what the rounding left (exact by FMA, plus the constant's own
 // tail): 2^p is the hardware's (2 ulp), the reciprocal too (1 ulp), and four
 // more roundings follow. g is taken as -87 below that, where e^-g nears the
 // end of fp32: the value is then below 1e-35 u, 0 beside any block maximum
 // that is not formed again in 64 bits.
-__device__ __forceinline__ float swiglu(float g, float u) {
-  constexpr float kLog2e = 1.44269504f;                            // log2(e) to fp32,
+__device__ __forceinline__ float2 swiglu2(float2 g, float2 u) {
+  constexpr float kLog2e = 1.44269504f;                                    // log2(e) to fp32,
   constexpr float kLog2eTail = (float)(1.4426950408889634 - 1.44269504f);  // and the rest
-  const float x = -fmaxf(g, -87.f);
-  const float p = x * kLog2e;
-  const float r = fmaf(x, kLog2eTail, fmaf(x, kLog2e, -p));
-  float e, inv;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(p));
-  e = fmaf(e * r, 0.693147181f, e);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(1.f + e));
-  return g * inv * u;
+  const float2 k = make_float2(-kLog2e, -kLog2e), k2 = make_float2(-kLog2eTail, -kLog2eTail);
+  const float2 x = make_float2(fmaxf(g.x, -87.f), fmaxf(g.y, -87.f));
+  const float2 p = __fmul2_rn(x, k);
+  const float2 r = __ffma2_rn(x, k2, __ffma2_rn(x, k, make_float2(-p.x, -p.y)));
+  float2 e, inv;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(p.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(p.y));
+  e = __ffma2_rn(__fmul2_rn(e, r), make_float2(0.693147181f, 0.693147181f), e);
+  const float2 d = __fadd2_rn(e, make_float2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.y) : "f"(d.y));
+  return __fmul2_rn(__fmul2_rn(g, inv), u);
 }
 // One lane's part of a block formed in 64 bits, for blocks whose scale fp32
 // cannot settle (a call: its registers are not the fast path's).
@@ -175,7 +177,7 @@ __device__ __noinline__ void swiglu64(const void* x, int64_t at, int cols, int n
   m = block_max(m);
   float inv;
   const float s = fp8_scale(m, &inv);
-  no_infinities(v, (float)m);
+  if (isinf((float)m)) no_infinities(v);
   if (row) put8(row, ld, c, v, inv);
   if (scale) *scale = s;
 }
@@ -199,7 +201,7 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
 // with one, a thread has 16 bytes of bf16 in flight. GATED: x is gate|up of
 // 2 * cols columns.
 template <bool BF16, bool VEC, bool GATED, int U>
-__global__ void __launch_bounds__(256) quantize_kernel(const void* __restrict__ x, uint32_t n_all, int cols,
+__global__ void __launch_bounds__(256, GATED ? 4 : 1) quantize_kernel(const void* __restrict__ x, uint32_t n_all, int cols,
                                                       FastDiv kb, int64_t ld, uint8_t* __restrict__ q,
                                                       float* __restrict__ scales) {
   pdl_launch_dependents();
@@ -229,7 +231,11 @@ __global__ void __launch_bounds__(256) quantize_kernel(const void* __restrict__ 
     float inv;
     if (GATED) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[k][j] = swiglu(g[k][j], v[k][j]);
+      for (int j = 0; j < 8; j += 2) {
+        const float2 h = swiglu2(make_float2(g[k][j], g[k][j + 1]), make_float2(v[k][j], v[k][j + 1]));
+        v[k][j] = h.x;
+        v[k][j + 1] = h.y;
+      }
     }
     const float amax = block_max(absmax8(v[k]));
     const float s = fp8_scale(amax, &inv);
@@ -239,7 +245,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const void* __restrict__ 
       swiglu64<BF16, VEC>(x, (int64_t)row[k] * 2 * cols + c[k], cols, i < n_all ? cols - c[k] : 0, out, ld, c[k], to);
       continue;
     }
-    no_infinities(v[k], amax);
+    if (!GATED && __any_sync(0xffffffffu, isinf(amax))) no_infinities(v[k]);
     if (out) put8(out, ld, c[k], v[k], inv);
     if (to) *to = s;
   }
@@ -273,13 +279,14 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t
   float h[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) h[j] = t[j] * rstd * g[j];
+  if (a.y) store8<true, VEC>(a.y, row * a.cols + c, n, h);  // (the same whether 8 bits are asked for or not)
   if (a.q) {
     float inv;
     const float amax = block_max(absmax8(h));
     float s = fp8_scale(amax, &inv);
     bool unsure = c - (int)(threadIdx.x & (kLanesPerBlock - 1)) * kVec < a.cols && fp8_scale_unsure(amax);
     if (__any_sync(0xffffffffu, unsure)) {
-      if (amax < 1e-30f) {  // tiny, or a block of zeros: nothing is unsure about that
+      if (amax < 1e-30f) {  // a block of zeros is sure
         float any = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) any = fmaxf(any, t[j] != 0.f && g[j] != 0.f ? 1.f : 0.f);
@@ -294,16 +301,15 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t
           m = fmax(m, fabs(e));
           h[j] = (float)e;
         }
-        s = fp8_scale(block_max(m), &inv);
+        m = block_max(m);
+        s = fp8_scale(m, &inv);
+        if (isinf((float)m)) no_infinities(h);
       }
     }
-    if (a.y) store8<true, VEC>(a.y, row * a.cols + c, n, h);
-    no_infinities(h, amax);
+    if (isinf(amax)) no_infinities(h);
     put8(a.q + row * ld, ld, c, h, inv);
     const int b = c / kFp8Block;
     if ((threadIdx.x & (kLanesPerBlock - 1)) == 0 && b < kb) a.scales[row * kb + b] = s;
-  } else {
-    store8<true, VEC>(a.y, row * a.cols + c, n, h);
   }
 }
 // 1 / sqrt of a mean of squares that may lie beyond the range of fp32.
@@ -317,9 +323,8 @@ __device__ __forceinline__ float root(double mean) {
 // own pieces of the next rows into shared memory (cp.async, D slots): a slot
 // is filled again after the next row's barrier, when no warp can still want
 // the row for its mean in 64 bits.
-// The kernel is bound by issue slots (48 instructions an element, most of them
-// per row and thread, made 8192 x 3584 take 56 us): so two chunks a thread,
-// sums in fp32 (17 roundings deep at most), and 64 bits only on demand.
+// Sums are fp32, in pairs (17 roundings deep at most), and 64 bits come on
+// demand. 8192 x 2048 fp32 rows with both outputs: 44 us, 5.7 TB/s.
 template <bool XBF16, bool RBF16, int NCH, int D>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs a, int64_t rows) {
   constexpr int XB = XBF16 ? 16 : 32, RB = RBF16 ? 16 : 32;  // bytes of 8 elements
@@ -499,6 +504,224 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
   }
 }
 
+// 8 values t of a bf16 row in shared memory: t = x + res, rounded to bf16:
+// what the next layer's residual holds and what the norm of the unfused
+// sequence would read; their 16 bytes come along as they are stored.
+__device__ __forceinline__ void load_sum(const uint8_t* xs, const uint8_t* rs, bool res, float (&v)[8], uint4& w) {
+  unpack8<true>(xs, v);
+  if (res) {
+    float r[8];
+    unpack8<true>(rs, r);
+    uint32_t u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * j] + r[2 * j], v[2 * j + 1] + r[2 * j + 1]);
+      u[j] = *reinterpret_cast<const uint32_t*>(&p);
+      v[2 * j] = __uint_as_float(u[j] << 16);
+      v[2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
+    }
+    w = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+}
+
+// bf16 rows of up to 16384 columns: rows blockIdx.x, + gridDim.x, ... one after
+// another. Four threads share a block of 128 columns: thread l of them has the
+// four pieces of 8 columns (4 k + l) 8 .., and their weights in registers. Each thread copies its own
+// pieces of the next rows into shared memory (cp.async, D slots); a slot is
+// filled again after the next row's barrier, when no warp can still want the
+// row for its mean in 64 bits.
+// The kernel is bound by issue slots: with one piece of a block per thread,
+// what is done once per block and thread (shuffles, scale, checks, addresses)
+// made 48 instructions an element, and 8192 x 3584 took 50 us, 40 with four.
+// (fp32 rows are better off in rmsnorm_kernel, 83 us for 8192 x 3584 against
+// 95 here: they are twice as long in shared memory, and fewer fit.)
+constexpr int kPieces = 4, kBf16Slots = 3;
+__global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t rows) {
+  constexpr int D = kBf16Slots, P = kPieces, L = kLanesPerBlock / P, kStep = L * kVec;  // threads of a block, columns from piece to piece
+  const int T = blockDim.x, tid = threadIdx.x, cols = a.cols;
+  const int64_t ld = fp8_ld(cols), step = gridDim.x;
+  const int kb = fp8_blocks(cols), half = T * 16;
+  extern __shared__ __align__(16) uint8_t ring[];  // [D][piece][T] of x, then of the residual
+  __shared__ float part[2][32];
+  pdl_launch_dependents();
+  const int blk = tid / L, c0 = blk * kFp8Block + tid % L * kVec;  // piece k starts at column c0 + kStep k
+  uint8_t* const xring = ring + tid * 16;
+  uint8_t* const rring = xring + (size_t)D * P * half;
+  auto xslot = [&](int d, int k) { return xring + (d * P + k) * half; };
+  auto rslot = [&](int d, int k) { return rring + (d * P + k) * half; };
+  const uint8_t* px = static_cast<const uint8_t*>(a.x) + ((int64_t)blockIdx.x * cols + c0) * 2;
+  const uint8_t* pr = static_cast<const uint8_t*>(a.res) + ((int64_t)blockIdx.x * cols + c0) * 2;
+  const int64_t xstep = step * cols * 2, rstep = step * cols * 2;
+  int64_t fetched = blockIdx.x;
+  auto fetch = [&](int d) {  // the next row into slot d
+    if (fetched < rows) {
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        if (c0 + kStep * k < cols) {
+          cp_async16(xslot(d, k), px + k * kStep * 2);
+          if (a.res) cp_async16(rslot(d, k), pr + k * kStep * 2);
+        }
+    }
+    fetched += step;
+    px += xstep;
+    pr += rstep;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  pdl_wait();
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d) fetch(d);
+  float g[P][8];
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    if (a.weight) {
+      load8<false, true>(a.weight, c0 + kStep * k, cols - c0 - kStep * k, g[k]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[k][j] = 1.f;
+    }
+  }
+  const float inv_cols = 1.f / (float)cols;
+  int flip = 0, d = 0;
+  for (int64_t row = blockIdx.x; row < rows; row += step, flip ^= 1) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");  // the oldest row
+    float t[P][8];
+    float2 sq = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      if (c0 + kStep * k < cols) {
+        uint4 w;
+        load_sum(xslot(d, k), rslot(d, k), a.res, t[k], w);
+        if (a.sum) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.sum) + row * cols + c0 + kStep * k) = w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[k][j] = 0.f;
+      }
+      // (two chains of at most 16 terms and 10 steps across lanes and warps: 27
+      // roundings deep at most, of positive terms)
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float2 v = make_float2(t[k][j], t[k][j + 1]);
+        sq = __ffma2_rn(v, v, sq);
+      }
+    }
+    float ss = sq.x + sq.y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if ((tid & 31) == 0) part[flip][tid >> 5] = ss;
+    __syncthreads();  // (the other half of `part` is written before the next barrier)
+    fetch(d == 0 ? D - 1 : d - 1);  // the last row's slot
+    ss = (tid & 31) < T / 32 ? part[flip][tid & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // the mean of squares (plus eps) in 64 bits, by one warp from shared memory
+    auto mean64 = [&]() {
+      double s = 0.0;
+#pragma unroll 1
+      for (int i = (tid & 31) - tid; i < T - tid; i += 32)  // thread tid + i's pieces
+#pragma unroll 1
+        for (int k = 0; k < P; ++k)
+          if ((tid + i) / L * kFp8Block + (tid + i) % L * kVec + kStep * k < cols) {
+            float v[8];
+            uint4 w;
+            load_sum(xslot(d, k) + i * 16, rslot(d, k) + i * 16, a.res, v, w);
+            for (int j = 0; j < 8; ++j) s = fma((double)v[j], (double)v[j], s);
+          }
+      for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      return s / cols + (double)a.eps;
+    };
+    const float mean = fmaf(ss, inv_cols, a.eps);
+    float rstd = root(mean);
+    if (!(mean < 1e37f && mean > 1e-30f)) rstd = root(mean64());  // squares beyond the range of fp32
+
+    // p = t g, its maximum over the block gives the scale; h = p rstd
+    float pm = 0.f;
+#pragma unroll
+    for (int k = 0; k < P; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        t[k][j] *= g[k][j];
+        pm = fmaxf(pm, fabsf(t[k][j]));
+      }
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, o));
+    const float amax = pm * rstd;
+    bool far = blk < kb && fp8_far(pm), in64 = false;  // (y is the same whether 8 bits are asked for or not)
+    bool unsure = far || (a.q && blk < kb && fp8_scale_unsure(amax));
+    if (__any_sync(0xffffffffu, unsure)) {
+      // a block of zeros is sure; the others of this warp are formed again in
+      // 64 bits, from shared memory
+      if (pm == 0.f) {
+        float any = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < P; ++k)
+          if (c0 + kStep * k < cols) {
+            float v[8];
+            uint4 w;
+            load_sum(xslot(d, k), rslot(d, k), a.res, v, w);
+            for (int j = 0; j < 8; ++j)
+              if (v[j] != 0.f && (!a.weight || __ldg(a.weight + c0 + kStep * k + j) != 0.f)) any = 1.f;
+          }
+        // (a block's threads are here together; each looks at its own pieces)
+        const uint32_t peers = ((1u << L) - 1) << (tid & 31 & ~(L - 1));
+        for (int o = 1; o < L; o <<= 1) any = fmaxf(any, __shfl_xor_sync(peers, any, o));
+        if (any == 0.f) far = unsure = false;
+      }
+      if (__any_sync(0xffffffffu, unsure)) {
+        const double r = 1.0 / sqrt(mean64());
+        double m = 0.0;
+        float inv = 1.f, s = 1.f;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+          for (int k = 0; k < P; ++k) {
+            const int c = c0 + kStep * k;
+            float v[8];
+            uint4 w;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+            if (c < cols) load_sum(xslot(d, k), rslot(d, k), a.res, v, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const double e = (double)v[j] * r * (a.weight && c < cols ? (double)__ldg(a.weight + c + j) : 1.0);
+              m = fmax(m, fabs(e));
+              v[j] = (float)e;
+            }
+            if (pass == 0) continue;
+            if (a.y && far) store8<true, true>(a.y, row * cols + c, cols - c, v);
+            if (isinf((float)m)) no_infinities(v);
+            if (a.q) put8(a.q + row * ld, ld, c, v, inv);
+          }
+          if (pass == 0) {
+#pragma unroll
+            for (int o = 1; o < L; o <<= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+            s = fp8_scale(m, &inv);
+          }
+        }
+        if (a.q && tid % L == 0 && blk < kb) a.scales[row * kb + blk] = s;
+        in64 = true;
+      }
+    }
+    if (a.y && !(in64 && far)) {
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        float h[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = t[k][j] * rstd;
+        store8<true, true>(a.y, row * cols + c0 + kStep * k, cols - c0 - kStep * k, h);
+      }
+    }
+    if (a.q && !in64) {
+      float inv;
+      const float s = fp8_scale(amax, &inv);
+      uint8_t* q = a.q + row * ld;
+#pragma unroll
+      for (int k = 0; k < P; ++k) put8(q, ld, c0 + kStep * k, t[k], rstd * inv);
+      if (tid % L == 0 && blk < kb) a.scales[row * kb + blk] = s;
+    }
+    d = d + 1 == D ? 0 : d + 1;
+  }
+}
+
 // One CTA per 128 x 128 block: warp w holds rows w, w + 8, ... (16 of them),
 // lane l the columns 4 l .. 4 l + 3, in registers between the maximum and the
 // output.
@@ -560,7 +783,8 @@ __global__ void __launch_bounds__(256, 2) encode_kernel(const void* __restrict__
   const float s = fp8_scale(m, &inv);
   if (threadIdx.x == 0) scales[blk] = s;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) no_infinities(v[i], m);
+  for (int i = 0; i < 16; ++i)
+    if (isinf(m)) no_infinities(v[i]);
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     const int r = rb * kFp8Block + i * 8 + warp;
@@ -661,26 +885,28 @@ cudaError_t resident(const void* kern, int t, size_t smem, int64_t* ctas) {
 
 template <bool XB, bool RB, bool VEC>
 cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t s) {
-  // chunks of 8 per row: one per thread up to 256 threads, then two of up to
-  // 1024, then rows that are read twice; as many CTAs as fit at once
+  // `pieces` of 8 columns per thread, `depth` rows in shared memory, as many
+  // CTAs as fit at once
   const int ch = (a.cols + kVec - 1) / kVec;
-  auto go = [&](auto kern, int nch, int depth) -> cudaError_t {
-    const int t = ((ch + nch - 1) / nch + 31) / 32 * 32;
-    const size_t smem = (size_t)depth * nch * t * ((XB ? 16 : 32) + (a.res ? RB ? 16 : 32 : 0));
+  auto go = [&](auto kern, int t, int pieces, int depth) -> cudaError_t {
+    t = (t + 31) / 32 * 32;
+    const size_t smem = (size_t)depth * pieces * t * ((XB ? 16 : 32) + (a.res ? RB ? 16 : 32 : 0));
     int64_t fit = 0;
     cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(kern));
     if (e == cudaSuccess) e = resident(reinterpret_cast<const void*>(kern), t, smem, &fit);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, (unsigned)std::min(rows, fit), (unsigned)t, smem, s, a, rows);
   };
-  if constexpr (VEC) {
-    if (ch <= 256) return go(rmsnorm_kernel<XB, RB, 1, 4>, 1, 4);
-    if (ch <= 1024) return go(rmsnorm_kernel<XB, RB, 2, 3>, 2, 3);
-    // (two rows of fp32 x and residual would take 2 * 2 * 1024 * 64 bytes)
-    if (ch <= 2048) return go(rmsnorm_kernel<XB, RB, 2, XB && RB ? 2 : 1>, 2, XB && RB ? 2 : 1);
+  if constexpr (VEC && XB && RB) {
+    const int t = fp8_blocks(a.cols) * (kLanesPerBlock / kPieces);
+    if (a.cols <= 16384) return go(rmsnorm_bf16_kernel, t, kPieces, kBf16Slots);
+  } else if constexpr (VEC) {
+    if (ch <= 256) return go(rmsnorm_kernel<XB, RB, 1, 4>, ch, 1, 4);
+    if (ch <= 1024) return go(rmsnorm_kernel<XB, RB, 2, 3>, (ch + 1) / 2, 2, 3);
+    if (ch <= 2048) return go(rmsnorm_kernel<XB, RB, 2, 1>, (ch + 1) / 2, 2, 1);
   }
-  const int t = std::min(1024, (ch + 31) / 32 * 32);
-  return launch_pdl(rmsnorm_long_kernel<XB, RB, VEC>, (unsigned)rows, (unsigned)t, 0, s, a);
+  return launch_pdl(rmsnorm_long_kernel<XB, RB, VEC>, (unsigned)rows, (unsigned)std::min(1024, (ch + 31) / 32 * 32), 0, s,
+                    a);
 }
 
 }  // namespace
