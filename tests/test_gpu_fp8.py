@@ -257,7 +257,8 @@ def test_rmsnorm_without_residual_or_weight(hxq, xt):
     check_y(y, h)
 
 
-def test_rmsnorm_extremes(hxq):
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+def test_rmsnorm_extremes(hxq, xt):
     """Rows of zeros, of values whose squares leave fp32's range, and with NaN or infinity; neighbours keep theirs."""
     x = randn(10, 8, 384)
     x[0] = 0
@@ -266,42 +267,95 @@ def test_rmsnorm_extremes(hxq):
     x[3, 5] = float("nan")
     x[4, 6] = float("inf")
     x[6] *= 3e37
+    x = x.to(dtype(xt))
     w = 1 + randn(11, 384, scale=0.1)
     w[128:256] = 0
     _, h = ref_norm(x, None, w, 0.0)
-    h[4] = np.nan  # infinity: the root is infinite, inf / inf is NaN and the others are 0
     _, h1 = ref_norm(x, None, w, 1e-6)
     q, s, y, _ = hxq.rmsnorm(x, w, 1e-6, want="qy")
     keep = [0, 1, 2, 5, 6, 7]
     check_bytes(q[keep], s[keep], h1[keep], 384, DELTA)
     check_y(y[keep], h1[keep])
-    assert np.isnan(f64(y)[3]).all()
-    yi = f64(y)[4]
+    assert np.isnan(f64(y)[3]).all() and ((codes(q)[3] & 0x7F) == 0x7F).all()
+    assert (f64(s)[3] == 1).all()  # nothing but NaN: no maximum
+    yi = f64(y)[4]  # the root is infinite: inf / inf is NaN and the others are 0
     assert np.isnan(yi[6]) and (np.delete(yi, 6) == 0).all()
-    y0 = f64(hxq.rmsnorm(x, w, 0.0, want="y")[2])
-    assert np.isnan(y0[0]).all()  # 0 / 0, as the formula says
-    check_y(hxq.rmsnorm(x, w, 0.0, want="y")[2][keep[1:]], h[keep[1:]])
+    assert (codes(q)[4, 6] & 0x7F) == 0x7F and not (np.delete(codes(q)[4], 6) & 0x7F).any()
+    q0, s0, y0, _ = hxq.rmsnorm(x, w, 0.0, want="qy")
+    assert np.isnan(f64(y0)[0]).all() and (f64(s0)[0] == 1).all()  # 0 / 0, as the formula says
+    check_y(y0[keep[1:]], h[keep[1:]])
+    check_bytes(q0[keep[1:]], s0[keep[1:]], h[keep[1:]], 384, DELTA)
 
 
-def test_rmsnorm_scales_at_their_borders(hxq):
-    """Rows whose largest |h| is 448 s or a rounding away from it: the scale is the one of the exact h."""
+@pytest.mark.parametrize("xt,K", [("f32", 256), ("bf16", 256), ("f32", 20000), ("bf16", 20000), ("bf16", 3592)])
+def test_rmsnorm_scales_at_their_borders(hxq, xt, K):
+    """Rows whose largest |h| is 448 s, or a few roundings of fp32 away from it: the scale is the one of the exact h.
+    Row r's largest value is in column r, whose weight is aimed at the border and nudged."""
     import torch
-    K, rows = 256, 64
+    rows = 64
     x = randn(12, rows, K)
+    x[torch.arange(rows), torch.arange(rows)] = 60.0 + torch.rand(rows, device="cuda")
+    x = x.to(dtype(xt))
+    w = 1 + randn(13, K, scale=0.1)
+    # the other rows' aimed columns are 0
+    col, row = torch.arange(K, device="cuda")[None], torch.arange(rows, device="cuda")[:, None]
+    x = torch.where((col < rows) & (col != row), torch.zeros_like(x), x)
     d = f64(x)
-    w = np.ones(K)
-    # weight of one column per row cannot differ, so aim the row's own largest value: t_j = 448 c with the
-    # other values chosen, then the mean fixes h; nudge by single bits around the border
+    root = np.sqrt((d * d).mean(1))
     for r in range(rows):
-        rest = (d[r, 1:] ** 2).sum()
-        # h_0 = v / sqrt((v^2 + rest) / K) = target -> v = target sqrt(rest / (K - target^2))
-        target = 14.0  # 448 / 32
-        v = np.float32(target * np.sqrt(rest / (K - target * target)))
-        x[r, 0] = float(np.nextafter(v, np.float32(np.inf if r % 2 else -np.inf))) if r % 3 else float(v)
-    _, h = ref_norm(x, None, None, 0.0)
-    assert (np.abs(h[:, 0] / 14.0 - 1) < 1e-6).all() and len(set(ref_scales(h)[:, 0])) == 2
-    q, s, _, _ = hxq.rmsnorm(x, torch.tensor(w, dtype=torch.float32, device="cuda"), 0.0)
+        g = np.float32(14.0 * root[r] / d[r, r])  # 14 = 448 / 32
+        for _ in range(abs(r % 9 - 4)):
+            g = np.nextafter(g, np.float32(np.inf if r % 9 > 4 else -np.inf))
+        w[r] = float(g)
+    _, h = ref_norm(x, None, w, 0.0)
+    assert (np.abs(h[np.arange(rows), np.arange(rows)] / 14.0 - 1) < 1e-6).all()
+    assert len(set(ref_scales(h)[:, 0])) == 2
+    q, s, _, _ = hxq.rmsnorm(x, w, 0.0)
     check_bytes(q, s, h, K, DELTA)
+
+
+def test_other_layouts_are_copied(hxq):
+    """A transposed and a sliced input give what their contiguous copies give; with a stream they are refused."""
+    import torch
+    base = randn(3, 200, 300)
+    st = torch.cuda.Stream()
+    for x in (base.t(), base[:, 7:263], base[::2]):
+        for f in (hxq.fp8_quantize, hxq.fp8_encode, lambda v, **k: hxq.rmsnorm(v, **k)[:2]):
+            a, b = f(x), f(x.contiguous())
+            assert torch.equal(codes_t(a[0]), codes_t(b[0])) and torch.equal(a[1], b[1])
+            with pytest.raises(hxq.HXQError):
+                f(x, stream=st)
+
+
+def test_row_operators_on_another_stream_and_captured(hxq):
+    """Each of them on a stream of its own behind the work that fills its input there, eager and as a graph."""
+    import torch
+    src = randn(4, 300, 1024)
+    x = torch.empty_like(src)
+    res = randn(5, 300, 1024)
+    calls = [lambda s: hxq.fp8_quantize(x, stream=s), lambda s: hxq.fp8_swiglu(x, stream=s),
+             lambda s: hxq.fp8_encode(x, stream=s), lambda s: hxq.rmsnorm(x, residual=res, want="qy", stream=s)]
+    x.copy_(src)
+    want = [[t.clone() for t in c(None) if t is not None] for c in calls]
+    torch.cuda.synchronize()
+    st = torch.cuda.Stream()
+    same = lambda a, b: torch.equal(a.view(torch.uint8), b.view(torch.uint8))  # noqa: E731
+    for c, w in zip(calls, want):
+        x.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            x.copy_(src)
+            got = [t for t in c(st) if t is not None]
+        st.synchronize()
+        assert all(same(a, b) for a, b in zip(got, w))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            x.copy_(src)
+            got = [t for t in c(None) if t is not None]
+        x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, w))
 
 
 # ---- products -----------------------------------------------------------------------
@@ -667,6 +721,8 @@ def test_handle_refusals(hxq):
                  lambda: hxq.fp8_swiglu(torch.zeros(2, 31, device="cuda")),
                  lambda: hxq.fp8_quantize(torch.zeros(2, 32, device="cuda", dtype=torch.float16)),
                  lambda: hxq.rmsnorm(x, residual=x[:2]), lambda: hxq.rmsnorm(x, sum_out=x),
+                 lambda: one.forward(xq.cpu(), xs.cpu(), y=y.cpu()), lambda: one.forward(xq, xs.cpu()),
+                 lambda: one.forward(xq, xs, y=y.cpu()), lambda: hxq.rmsnorm(x, scales=xs, want="y"),
                  lambda: hxq.rmsnorm(x, torch.ones(31, device="cuda")), lambda: hxq.rmsnorm(x, want="z")):
         with pytest.raises(hxq.HXQError) as e:
             call()

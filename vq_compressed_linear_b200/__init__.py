@@ -490,12 +490,18 @@ def _raw(stream, device: int):
     return _torch.raw_stream(device) if stream is None else int(getattr(stream, "cuda_stream", stream))
 
 
-def _input(t, dims: int, what: str):
-    """`t` contiguous and its HXQ_TYPE_*: float32 or bfloat16 on the current CUDA device."""
+def _input(t, dims: int, stream, what: str):
+    """`t` contiguous and its HXQ_TYPE_*: float32 or bfloat16 on the current
+    CUDA device. Other layouts are copied, on the current stream: with a
+    stream given they are refused, since nothing would order the two."""
     code = _t().code.get(t.dtype)
     if code is None or not t.is_cuda or t.dim() != dims or t.get_device() != _torch.device():
         _refuse(f"{what}: a {dims}D float32 or bfloat16 tensor on the current CUDA device")
-    return (t if t.is_contiguous() else t.contiguous()), code
+    if t.is_contiguous():
+        return t, code
+    if stream is not None:
+        _refuse(f"{what}: a contiguous tensor, where a stream is given")
+    return t.contiguous(), code
 
 
 def _output(t, shape, dtype, device: int, what: str):
@@ -515,7 +521,7 @@ def _bytes(t, shape, device: int, what: str):
 def fp8_quantize(x, q=None, scales=None, stream=None):
     """x [M, K] (float32 or bfloat16 CUDA) as an 8-bit activation. Returns
     (q float8_e4m3fn [M, K rounded up to 16], scales float32 [M, ceil(K / 128)])."""
-    x, code = _input(x, 2, "fp8_quantize")
+    x, code = _input(x, 2, stream, "fp8_quantize")
     (rows, cols), dev = x.shape, x.get_device()
     q = _bytes(q, (rows, (cols + 15) // 16 * 16), dev, "fp8_quantize: q")
     scales = _output(scales, (rows, (cols + 127) // 128), _torch.f32, dev, "fp8_quantize: scales")
@@ -527,7 +533,7 @@ def fp8_quantize(x, q=None, scales=None, stream=None):
 def fp8_swiglu(gate_up, q=None, scales=None, stream=None):
     """silu(gate) * up of gate_up [M, 2 K] (gate first) as an 8-bit
     activation [M, K]; returns (q, scales) as fp8_quantize."""
-    x, code = _input(gate_up, 2, "fp8_swiglu")
+    x, code = _input(gate_up, 2, stream, "fp8_swiglu")
     (rows, both), dev = x.shape, x.get_device()
     if both % 2:
         _refuse("fp8_swiglu: gate_up is [M, 2 K]")
@@ -543,7 +549,7 @@ def fp8_encode(W, q=None, scales=None, stream=None):
     """Weights [N, K] or [E, N, K] (float32 or bfloat16 CUDA) as 8-bit values
     of the same shape and scales [(E,) ceil(N / 128), ceil(K / 128)]: what
     Fp8Linear takes."""
-    W, code = _input(W, 3 if W.dim() == 3 else 2, "fp8_encode")
+    W, code = _input(W, 3 if W.dim() == 3 else 2, stream, "fp8_encode")
     dev, (N, K) = W.get_device(), W.shape[-2:]
     q = _bytes(q, W.shape, dev, "fp8_encode: q")
     scales = _output(scales, (*W.shape[:-2], (N + 127) // 128, (K + 127) // 128), _torch.f32, dev, "fp8_encode: scales")
@@ -562,7 +568,7 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=Non
     given of y and q (q if neither is). sum_out receives t (it may be the
     residual itself; a new tensor if there is a residual and none is given).
     Returns (q, scales, y, sum), None for what was not asked for."""
-    x, xt = _input(x, 2, "rmsnorm")
+    x, xt = _input(x, 2, stream, "rmsnorm")
     T = _torch
     shape, dev = x.shape, x.get_device()
     rows, cols = shape
@@ -575,7 +581,7 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=Non
     rp = sp = wp = yp = qp = cp = None
     rt = xt
     if residual is not None:
-        residual, rt = _input(residual, 2, "rmsnorm: residual")
+        residual, rt = _input(residual, 2, stream, "rmsnorm: residual")
         if residual.shape != shape:
             _refuse("rmsnorm: residual has the shape of x")
         sum_out = _output(sum_out, shape, residual.dtype, dev, "rmsnorm: sum_out")
@@ -616,6 +622,7 @@ class Fp8Linear:
         if scales.dtype is not T.f32 or scales.shape != (*W.shape[:-2], (self.N + 127) // 128, self._kb):
             _refuse("Fp8Linear: scales are float32, one per 128 x 128 block")
         self.handle = hxq_fp8_create(W.contiguous(), scales.contiguous(), self.E, self.N, self.K)
+        self._dev = T.device()
 
     @classmethod
     def from_weight(cls, W) -> "Fp8Linear":
@@ -625,8 +632,8 @@ class Fp8Linear:
     def _args(self, xq, xs, bias, out_dtype, y, stream):
         T = _torch
         M, dev = xq.shape[0], xq.get_device()
-        if dev < 0:
-            _refuse("Fp8Linear: xq is a CUDA tensor")
+        if dev != self._dev:
+            _refuse(f"Fp8Linear: xq is on the weights' device, CUDA device {self._dev}")
         _bytes(xq, (M, self._ld), dev, "Fp8Linear: xq")
         _output(xs, (M, self._kb), T.f32, dev, "Fp8Linear: xs")
         bp = None

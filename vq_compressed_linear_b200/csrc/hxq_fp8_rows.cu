@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
       }
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) pm = fmaxf(pm, __shfl_xor_sync(0xffffffffu, pm, o));
-    const float amax = pm * rstd;
+    const float amax = fmaxf(pm * rstd, 0.f);  // (a row of NaN has no maximum)
     bool far = blk < kb && fp8_far(pm), in64 = false;  // (y is the same whether 8 bits are asked for or not)
     bool unsure = far || (a.q && blk < kb && fp8_scale_unsure(amax));
     if (__any_sync(0xffffffffu, unsure)) {
