@@ -508,14 +508,16 @@ def _output(t, shape, dtype, device: int, what: str):
     """`t`, checked, or a new tensor of that shape and type."""
     if t is None:
         return _torch.empty(shape, dtype=dtype, device=device)
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
         _refuse(f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {device}")
     return t
 
 
 def _bytes(t, shape, device: int, what: str):
     """As _output for 8-bit values, which may also come as uint8."""
-    return _output(t, shape, _torch.q if t is None or t.dtype is not _torch.q8[1] else t.dtype, device, what)
+    if t is None or t.dtype is _torch.q:
+        return _output(t, shape, _torch.q, device, what)
+    return _output(t, shape, _torch.q8[1], device, what)
 
 
 def fp8_quantize(x, q=None, scales=None, stream=None):
@@ -569,6 +571,7 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=Non
     residual itself; a new tensor if there is a residual and none is given).
     Returns (q, scales, y, sum), None for what was not asked for."""
     x, xt = _input(x, 2, stream, "rmsnorm")
+    rt = xt
     T = _torch
     shape, dev = x.shape, x.get_device()
     rows, cols = shape
@@ -579,11 +582,12 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=Non
         if want not in ("q", "y", "qy", "yq") or (y is not None and not want_y) or (q is not None and not want_q):
             _refuse("rmsnorm: want is 'q', 'y' or 'qy', and covers the outputs that are given")
     rp = sp = wp = yp = qp = cp = None
-    rt = xt
     if residual is not None:
-        residual, rt = _input(residual, 2, stream, "rmsnorm: residual")
-        if residual.shape != shape:
-            _refuse("rmsnorm: residual has the shape of x")
+        if residual.dtype is not x.dtype or residual.shape != shape or not residual.is_contiguous() or \
+                residual.get_device() != dev:  # (not the common case)
+            residual, rt = _input(residual, 2, stream, "rmsnorm: residual")
+            if residual.shape != shape:
+                _refuse("rmsnorm: residual has the shape of x")
         sum_out = _output(sum_out, shape, residual.dtype, dev, "rmsnorm: sum_out")
         rp, sp = residual.data_ptr(), sum_out.data_ptr()
     elif sum_out is not None:
@@ -599,8 +603,10 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=Non
     if want_y:
         y = _output(y, shape, T.bf16, dev, "rmsnorm: y")
         yp = y.data_ptr()
-    _check(lib.hxq_rmsnorm(x.data_ptr(), xt, rp, sp, rt, wp, eps, rows, cols, yp, qp, cp, _raw(stream, dev)),
-           "hxq_rmsnorm")
+    rc = lib.hxq_rmsnorm(x.data_ptr(), xt, rp, sp, rt, wp, eps, rows, cols, yp, qp, cp,
+                         T.raw_stream(dev) if stream is None else _raw(stream, dev))
+    if rc:
+        raise HXQError(rc, "hxq_rmsnorm")
     return q, scales, y, sum_out
 
 

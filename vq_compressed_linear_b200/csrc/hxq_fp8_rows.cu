@@ -852,7 +852,8 @@ cudaError_t launch_quant(const void* x, int bf16, int64_t rows, int cols, uint8_
 }
 
 // CTAs of `kern` with t threads and smem bytes of dynamic shared memory that
-// are resident on the current device at once, asked once for each.
+// are resident on the current device at once, asked once for each (which also
+// lets the kernel have that much shared memory).
 cudaError_t resident(const void* kern, int t, size_t smem, int64_t* ctas) {
   struct Known {
     int device;
@@ -872,7 +873,8 @@ cudaError_t resident(const void* kern, int t, size_t smem, int64_t* ctas) {
       *ctas = k.ctas;
       return cudaSuccess;
     }
-  if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, t, smem)) != cudaSuccess ||
+  if ((e = allow_max_smem(kern)) != cudaSuccess ||
+      (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kern, t, smem)) != cudaSuccess ||
       (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
   *ctas = (int64_t)std::max(1, per) * sms;
@@ -892,8 +894,7 @@ cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t s) {
     t = (t + 31) / 32 * 32;
     const size_t smem = (size_t)depth * pieces * t * ((XB ? 16 : 32) + (a.res ? RB ? 16 : 32 : 0));
     int64_t fit = 0;
-    cudaError_t e = allow_max_smem(reinterpret_cast<const void*>(kern));
-    if (e == cudaSuccess) e = resident(reinterpret_cast<const void*>(kern), t, smem, &fit);
+    const cudaError_t e = resident(reinterpret_cast<const void*>(kern), t, smem, &fit);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, (unsigned)std::min(rows, fit), (unsigned)t, smem, s, a, rows);
   };
