@@ -312,10 +312,13 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t
     if ((threadIdx.x & (kLanesPerBlock - 1)) == 0 && b < kb) a.scales[row * kb + b] = s;
   }
 }
-// 1 / sqrt of a mean of squares that may lie beyond the range of fp32.
-__device__ __forceinline__ float root(float mean) { return rsqrtf(mean); }
+// 1 / sqrt of a mean of squares, which may lie beyond the range of fp32: the
+// hardware's root (2 ulp, the same for a whole row, and enough to turn some
+// bytes) with one Newton step, its residual in 64 bits.
 __device__ __forceinline__ float root(double mean) {
-  return mean > 1e37 || mean < 1e-37 ? (float)(1.0 / sqrt(mean)) : rsqrtf((float)mean);
+  if (!(mean < 1e37 && mean > 1e-37)) return (float)(1.0 / sqrt(mean));
+  const float r = rsqrtf((float)mean);
+  return fmaf(0.5f * r, (float)fma(-mean * r, (double)r, 1.0), r);
 }
 
 // Rows blockIdx.x, + gridDim.x, ... one after another; thread t has the columns
@@ -323,8 +326,9 @@ __device__ __forceinline__ float root(double mean) {
 // own pieces of the next rows into shared memory (cp.async, D slots): a slot
 // is filled again after the next row's barrier, when no warp can still want
 // the row for its mean in 64 bits.
-// Sums are fp32, in pairs (17 roundings deep at most), and 64 bits come on
-// demand. 8192 x 2048 fp32 rows with both outputs: 44 us, 5.7 TB/s.
+// Sums are fp32 in a warp (9 roundings deep at most) and 64 bits across warps;
+// other 64 bits come on demand. 8192 x 2048 fp32 rows with both
+// outputs: 43 us, 5.9 TB/s.
 template <bool XBF16, bool RBF16, int NCH, int D>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs a, int64_t rows) {
   constexpr int XB = XBF16 ? 16 : 32, RB = RBF16 ? 16 : 32;  // bytes of 8 elements
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs
       for (int j = 0; j < 8; ++j) g[i][j] = 1.f;
     }
   }
-  const float inv_cols = 1.f / (float)cols;
+  const double inv_cols = 1.0 / cols;
   int flip = 0, d = 0;
   for (int64_t row = blockIdx.x; row < rows; row += step, flip ^= 1) {
     asm volatile("cp.async.wait_group %0;" ::"n"(D > 1 ? D - 2 : 0) : "memory");  // the oldest row
@@ -426,9 +430,9 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs
     if ((tid & 31) == 0) part[flip][tid >> 5] = ss;
     __syncthreads();  // (the other half of `part` is written before the next barrier)
     if (D > 1) fetch(d == 0 ? D - 1 : d - 1);  // the last row's slot
-    ss = (tid & 31) < T / 32 ? part[flip][tid & 31] : 0.f;
+    double sd = (tid & 31) < T / 32 ? (double)part[flip][tid & 31] : 0.0;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    for (int o = 16; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
     // the row's mean of squares in 64 bits, by one warp from shared memory
     auto mean64 = [&]() {
       double s64 = 0.0;
@@ -441,9 +445,9 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs
       for (int o = 16; o; o >>= 1) s64 += __shfl_xor_sync(0xffffffffu, s64, o);
       return s64 / cols + (double)a.eps;
     };
-    const float mean = fmaf(ss, inv_cols, a.eps);
+    const double mean = fma(sd, inv_cols, (double)a.eps);
     float rstd = root(mean);
-    if (!(mean < 1e37f && mean > 1e-30f)) rstd = root(mean64());  // squares beyond the range of fp32
+    if (!(mean < 1e37 && mean > 1e-30)) rstd = root(mean64());  // squares beyond the range of fp32
 #pragma unroll
     for (int i = 0; i < NCH; ++i) norm_out<true>(a, row, ld, kb, col(i), t[i], g[i], rstd, mean64);
     if (D == 1) {
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
       for (int j = 0; j < 8; ++j) g[k][j] = 1.f;
     }
   }
-  const float inv_cols = 1.f / (float)cols;
+  const double inv_cols = 1.0 / cols;
   int flip = 0, d = 0;
   for (int64_t row = blockIdx.x; row < rows; row += step, flip ^= 1) {
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 2) : "memory");  // the oldest row
@@ -596,8 +600,8 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
 #pragma unroll
         for (int j = 0; j < 8; ++j) t[k][j] = 0.f;
       }
-      // (two chains of at most 16 terms and 10 steps across lanes and warps: 27
-      // roundings deep at most, of positive terms)
+      // (two chains of 16 terms and 6 steps across lanes: 22 roundings deep at
+      // most, of positive terms)
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const float2 v = make_float2(t[k][j], t[k][j + 1]);
@@ -610,9 +614,9 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
     if ((tid & 31) == 0) part[flip][tid >> 5] = ss;
     __syncthreads();  // (the other half of `part` is written before the next barrier)
     fetch(d == 0 ? D - 1 : d - 1);  // the last row's slot
-    ss = (tid & 31) < T / 32 ? part[flip][tid & 31] : 0.f;
+    double sd = (tid & 15) < T / 32 ? (double)part[flip][tid & 15] : 0.0;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    for (int o = 8; o; o >>= 1) sd += __shfl_xor_sync(0xffffffffu, sd, o);
     // the mean of squares (plus eps) in 64 bits, by one warp from shared memory
     auto mean64 = [&]() {
       double s = 0.0;
@@ -629,9 +633,9 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
       for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       return s / cols + (double)a.eps;
     };
-    const float mean = fmaf(ss, inv_cols, a.eps);
+    const double mean = fma(sd, inv_cols, (double)a.eps);
     float rstd = root(mean);
-    if (!(mean < 1e37f && mean > 1e-30f)) rstd = root(mean64());  // squares beyond the range of fp32
+    if (!(mean < 1e37 && mean > 1e-30)) rstd = root(mean64());  // squares beyond the range of fp32
 
     // p = t g, its maximum over the block gives the scale; h = p rstd
     float pm = 0.f;
