@@ -9,20 +9,15 @@
 // back and added to fp32 accumulators in registers, times its two scales.
 // Products of e4m3 values carry 8 significand bits and are exact in fp32.
 //
-// fp8_skinny_kernel: D = W . x^T, lanes = 128 output features, columns = BN
-// tokens. Bound by the weights' bytes for few tokens. The unit of work is
-// (expert, 128-row tile of W, block of BN tokens); a cluster of CTAs shares a
-// unit's K, each CTA streaming its part of the tile row with TMA, and the
-// partial sums meet in distributed shared memory: rank r adds the columns it
-// owns in rank order, so results are bitwise repeatable and no global
-// workspace exists. The units are numbered token block fastest (token blocks
-// of one tile run side by side and share it in L2) and taken round robin by a
-// persistent grid.
-//
-// Warps: 0 TMA loads, 1 MMA issue, 2 TMEM, 3 activation scales (cp.async
-// into the ring slot of their block), 4..7 epilogue. Every wait is bounded:
-// on timeout the CTA sets a status bit, drains what it issued, frees TMEM
-// and returns.
+// Two kernels: fp8_skinny_kernel for few tokens, bound by the weights' bytes,
+// fp8_wide_kernel for many, bound by the tensor cores and the adding; which one
+// runs is estimated from the call's sizes (launch_mm). In both, one warp loads
+// by TMA, one issues MMAs, one owns TMEM, one brings the activation scales
+// (cp.async into a ring), and the others read P_b, add and store. The issuing
+// warps run converged and issue through one elected lane: from `if (lane ==
+// 0)`, an MMA took 72 cycles to issue instead of 35. Every wait is bounded: on
+// timeout the CTA sets a status bit, drains what it issued, frees TMEM and
+// returns.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -89,10 +84,8 @@ __device__ __forceinline__ void mbar_signal_rank(uint64_t* bar, uint32_t rank) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
                ::"r"(map_to_rank(smem_u32(bar), rank)) : "memory");
 }
-// Waits, bounded at kWaitCycles (about 2 s): false, with *abort set, when the
-// limit passes or another thread of the CTA gave up. The limit is counted in
-// SM cycles: reading %globaltimer costs more than an ordinary wait here takes
-// (measured below).
+// Waits, bounded at kWaitCycles of the SM's clock (about 2 s): false, with
+// *abort set, when the limit passes or another thread of the CTA gave up.
 constexpr long long kWaitCycles = 4000000000ll;
 
 template <bool CLUSTER>
@@ -218,6 +211,18 @@ struct Walk {
 };
 
 // ---- few tokens ---------------------------------------------------------------
+//
+// fp8_skinny_kernel: D = W . x^T, lanes = 128 output features, columns = BN
+// tokens. The unit of work is (expert, 128-row tile of W, block of BN tokens),
+// token blocks fastest (those of one tile run side by side and share it in
+// L2), taken round robin by a persistent grid. A cluster of CTAs shares a
+// unit's K; the partial sums meet in distributed shared memory, where rank r
+// adds the columns it owns in rank order: bitwise repeatable, and no global
+// workspace. The scale of a column (its token's) comes from shared memory, four
+// columns a load, the tile's is one factor more.
+// 1 x 11008 x 2048 in 7.1 us (3.2 TB/s of weights), 29 x 2048 x 11008 in 9.3:
+// the start (1 us to the first bytes), the last stage's way out and the
+// cluster's exchange (2 us) weigh as much as the 3.5 us that HBM needs.
 
 template <int BN>
 struct Sk {
@@ -642,11 +647,13 @@ cudaError_t launch_skinny(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, 
 // tile's), so adding P_b is one multiply-add per element.
 //
 // P_b has two buffers in TMEM. Eight warps read it, each 32 tokens x half the
-// features, in pieces of 32 columns: the next piece (of this block of K or
-// the next) loads while the last one is added, and a buffer is handed back
-// once its last piece has been read. (Halves of 128 features with an MMA and
-// buffers of their own were slower, 126 us against 113 for 2048 x 14336 x
-// 3584: an MMA of 128 columns reads its 256 tokens as often as one of 256.)
+// features, 64 columns at a time, and hand it back before they add the last
+// ones. A block of K takes 775 cycles against the MMAs' 512: the way round a
+// buffer (MMA, commit, read, arrival in the leading CTA, issue) takes 1550.
+// 2048 x 14336 x 3584 runs in 111 us, 1.9 PFLOP/s. Tried and slower there:
+// halves of 128 features with an MMA and buffers of their own, 126 us (their
+// MMAs read the 256 tokens from shared memory twice); 16 adding warps, 127;
+// reads of 32 columns, each under way while the last one is added, 122.
 //
 // The units are (expert, 256 tokens, two tiles of W), one after another on
 // each pair, in groups of 8 token blocks that walk the features together (so
