@@ -541,6 +541,52 @@ def test_grouped_survives_bad_offsets(hxq, M):
     lin.check()
 
 
+# ---- sizes past 32 bits ------------------------------------------------------------
+
+def test_more_than_2_31_outputs(hxq):
+    """y of 2.2e9 elements: rows at both ends and around element 2^31."""
+    import torch
+    M, N, K = 55000, 40016, 144
+    xq, xs = make_activation(1, M, K)
+    wq, ws = make_weights(2, 1, N, K)
+    y = hxq.Fp8Linear(wq[0], ws[0]).forward(xq, xs, out_dtype=hxq.HXQ_OUT_BF16)
+    w = dense_w(wq[0], ws[0])
+    mid = 2**31 // N
+    for r in (slice(0, 40), slice(mid - 20, mid + 20), slice(M - 40, M)):
+        check_product(y[r], dense_x(xq[r], xs[r], K), w, None, f"rows {r}")
+
+
+def test_more_than_2_31_weights(hxq):
+    """Experts whose weights take 2.3 GB: the first and the last, few rows and many."""
+    import torch
+    E, N, K = 34, 8200, 8208
+    wq = torch.empty(E, N, K, dtype=torch.float8_e4m3fn, device="cuda")
+    for e in range(E):
+        wq[e] = randn(e, N, K, scale=100.0).clamp_(-448, 448).to(torch.float8_e4m3fn)
+    ws = 3e-4 * torch.exp(randn(99, E, 65, 65))
+    lin = hxq.Fp8Linear(wq, ws)
+    for n in (3, 300):
+        xq, xs = make_activation(5, 2 * n, K)
+        y = lin.forward_grouped(xq, xs, offsets_of([n] + [0] * (E - 2) + [n]))
+        for e, r in ((0, slice(0, n)), (E - 1, slice(n, 2 * n))):
+            check_product(y[r], dense_x(xq[r], xs[r], K), dense_w(wq[e], ws[e]), None, f"expert {e}")
+
+
+def test_more_than_2_31_elements_quantized(hxq):
+    import torch
+    M, K = 70001, 32000
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_()
+    mid = 2**31 // K
+    rows = [0, 1, mid - 1, mid, mid + 1, M - 1]
+    q, s = hxq.fp8_quantize(x)
+    check_bytes(q[rows], s[rows], f64(x[rows]), K)
+    del q, s
+    x = x.view(-1)[:2**31 + 2**20].view(-1, 16384)  # 131136 rows
+    q, s, _, _ = hxq.rmsnorm(x)
+    rows = [0, 131071, 131072, x.shape[0] - 1]
+    check_bytes(q[rows], s[rows], ref_norm(x[rows], None, None, 1e-6)[1], 16384, DELTA)
+
+
 # ---- streams, graphs, refusals -----------------------------------------------------------
 
 def test_zero_rows(hxq):
