@@ -159,26 +159,36 @@ __device__ __forceinline__ float2 swiglu2(float2 g, float2 u) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.y) : "f"(d.y));
   return __fmul2_rn(__fmul2_rn(g, inv), u);
 }
-// One lane's part of a block formed in 64 bits, for blocks whose scale fp32
-// cannot settle (a call: its registers are not the fast path's).
+// One thread's part of a block (8 columns from c0 + 8 lanes k on for each of
+// its `pieces`, `lanes` threads a block) formed in 64 bits, for blocks whose scale
+// fp32 cannot settle (a call: its registers are not the fast path's). at: the
+// gate of column c0; n: columns from c0 on.
 template <bool BF16, bool VEC>
-__device__ __noinline__ void swiglu64(const void* x, int64_t at, int cols, int n, uint8_t* row, int64_t ld, int c,
-                                      float* scale) {
-  float g[8], v[8];
-  load8<BF16, VEC>(x, at, n, g);
-  load8<BF16, VEC>(x, at + cols, n, v);
+__device__ __noinline__ void swiglu64(const void* x, int64_t at, int cols, int n, uint8_t* row, int64_t ld, int c0,
+                                      int pieces, int lanes, float* scale) {
   double m = 0.0;
+  float inv = 1.f, s = 1.f;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int k = 0; k < pieces; ++k) {
+      float g[8], v[8];
+      load8<BF16, VEC>(x, at + 8 * lanes * k, n - 8 * lanes * k, g);
+      load8<BF16, VEC>(x, at + cols + 8 * lanes * k, n - 8 * lanes * k, v);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const double d = (double)g[j] / (1.0 + exp(-(double)g[j])) * (double)v[j];
-    m = fmax(m, fabs(d));
-    v[j] = (float)d;
+      for (int j = 0; j < 8; ++j) {
+        const double d = (double)g[j] / (1.0 + exp(-(double)g[j])) * (double)v[j];
+        m = fmax(m, fabs(d));
+        v[j] = (float)d;
+      }
+      if (pass == 1) {
+        if (isinf((float)m)) no_infinities(v);
+        if (row) put8(row, ld, c0 + 8 * lanes * k, v, inv);
+      }
+    }
+    if (pass == 0) {
+      for (int o = 1; o < lanes; o <<= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+      s = fp8_scale(m, &inv);
+    }
   }
-  m = block_max(m);
-  float inv;
-  const float s = fp8_scale(m, &inv);
-  if (isinf((float)m)) no_infinities(v);
-  if (row) put8(row, ld, c, v, inv);
   if (scale) *scale = s;
 }
 
@@ -196,59 +206,129 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
   return f.s ? __umulhi(n, f.m) >> (f.s - 1) : n;
 }
 
-// One half-warp per block of 128, blocks numbered row-major, U of them per
-// half-warp (16 U CTA-wide apart), all loaded before the first is worked on:
-// with one, a thread has 16 bytes of bf16 in flight. GATED: x is gate|up of
-// 2 * cols columns.
-template <bool BF16, bool VEC, bool GATED, int U>
-__global__ void __launch_bounds__(256, GATED ? 4 : 1) quantize_kernel(const void* __restrict__ x, uint32_t n_all, int cols,
-                                                      FastDiv kb, int64_t ld, uint8_t* __restrict__ q,
+// A thread's 8 elements as they lie in memory.
+template <bool BF16>
+struct Raw8 {
+  uint4 w[BF16 ? 1 : 2];
+};
+template <bool BF16>
+__device__ __forceinline__ Raw8<BF16> load_raw(const void* base, int64_t at, bool live) {
+  Raw8<BF16> r;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(base) + at * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int k = 0; k < (BF16 ? 1 : 2); ++k) r.w[k] = live ? p[k] : make_uint4(0, 0, 0, 0);
+  return r;
+}
+template <bool BF16>
+__device__ __forceinline__ void unpack(const Raw8<BF16>& r, float (&v)[8]) {
+  const uint32_t* u = reinterpret_cast<const uint32_t*>(r.w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = __uint_as_float(!BF16 ? u[j] : j & 1 ? u[j / 2] & 0xFFFF0000u : u[j / 2] << 16);
+}
+
+// L = 16 / P threads per block of 128, blocks numbered row-major; thread l of
+// them has the P pieces of 8 columns (L k + l) 8 .., all loaded before the
+// first is worked on. GATED: x is gate|up of 2 * cols columns. Rows of whole
+// 16-byte pieces. More pieces pay less often for what is done once per block
+// and thread (shuffles, scale, addresses), and hold more registers: plain
+// 2048 x 14336 bf16 takes 14.1 us with four (6.3 TB/s) and 17.6 with one,
+// gated 30.8 with two (bound by issue slots; fp32 41, 6.4 TB/s) and 37 with
+// four or one.
+template <bool BF16, bool GATED>
+__global__ void __launch_bounds__(256) quantize_kernel(const void* __restrict__ x, uint32_t n_all, int cols, FastDiv kb,
+                                                      int64_t ld, uint8_t* __restrict__ q,
                                                       float* __restrict__ scales) {
+  constexpr int P = GATED ? 2 : 4, L = kLanesPerBlock / P, kStep = L * kVec;  // pieces, threads of a block
   pdl_launch_dependents();
   pdl_wait();
-  const int sub = threadIdx.x & (kLanesPerBlock - 1);
   // whole warps take part in the shuffles: a block past the end has no columns
-  const uint32_t i0 = blockIdx.x * (16 * U) + threadIdx.x / kLanesPerBlock;
-  float v[U][8], g[GATED ? U : 1][8];
-  uint32_t row[U];
-  int c[U];
+  const uint32_t i = blockIdx.x * (256 / L) + threadIdx.x / L;
+  const bool live = i < n_all;
+  const uint32_t row = div_by(i, kb);
+  const int c0 = (int)(i - row * kb.d) * kFp8Block + threadIdx.x % L * kVec;
+  const int n = live ? cols - c0 : 0;
+  const int64_t at = (int64_t)row * cols * (GATED ? 2 : 1) + c0;
+  Raw8<BF16> ra[P], rb[GATED ? P : 1];
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const uint32_t i = i0 + k * 16;
-    row[k] = div_by(i, kb);
-    c[k] = (int)(i - row[k] * kb.d) * kFp8Block + sub * kVec;
-    const int n = i < n_all ? cols - c[k] : 0;
-    if (GATED) {
-      load8<BF16, VEC>(x, (int64_t)row[k] * 2 * cols + c[k], n, g[k]);
-      load8<BF16, VEC>(x, (int64_t)row[k] * 2 * cols + cols + c[k], n, v[k]);
-    } else {
-      load8<BF16, VEC>(x, (int64_t)row[k] * cols + c[k], n, v[k]);
-    }
+  for (int k = 0; k < P; ++k) {
+    ra[k] = load_raw<BF16>(x, at + kStep * k, kStep * k < n);
+    if (GATED) rb[k] = load_raw<BF16>(x, at + cols + kStep * k, kStep * k < n);
   }
+  float v[P][8], amax = 0.f;
 #pragma unroll
-  for (int k = 0; k < U; ++k) {
-    const uint32_t i = i0 + k * 16;
-    float inv;
+  for (int k = 0; k < P; ++k) {
+    unpack<BF16>(ra[k], v[k]);
     if (GATED) {
+      float u[8];
+      unpack<BF16>(rb[k], u);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        const float2 h = swiglu2(make_float2(g[k][j], g[k][j + 1]), make_float2(v[k][j], v[k][j + 1]));
+        const float2 h = swiglu2(make_float2(v[k][j], v[k][j + 1]), make_float2(u[j], u[j + 1]));
         v[k][j] = h.x;
         v[k][j + 1] = h.y;
       }
     }
-    const float amax = block_max(absmax8(v[k]));
-    const float s = fp8_scale(amax, &inv);
-    uint8_t* out = i < n_all ? q + row[k] * ld : nullptr;
-    float* to = i < n_all && sub == 0 ? scales + i : nullptr;
-    if (GATED && __any_sync(0xffffffffu, i < n_all && fp8_scale_unsure(amax))) {
-      swiglu64<BF16, VEC>(x, (int64_t)row[k] * 2 * cols + c[k], cols, i < n_all ? cols - c[k] : 0, out, ld, c[k], to);
-      continue;
-    }
-    if (!GATED && __any_sync(0xffffffffu, isinf(amax))) no_infinities(v[k]);
-    if (out) put8(out, ld, c[k], v[k], inv);
-    if (to) *to = s;
+    amax = fmaxf(amax, absmax8(v[k]));
   }
+#pragma unroll
+  for (int o = 1; o < L; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  uint8_t* out = live ? q + row * ld : nullptr;
+  float* to = live && threadIdx.x % L == 0 ? scales + i : nullptr;
+  if (GATED && __any_sync(0xffffffffu, live && fp8_scale_unsure(amax))) {
+    swiglu64<BF16, true>(x, at, cols, n, out, ld, c0, P, L, to);
+    return;
+  }
+  float inv;
+  const float s = fp8_scale(amax, &inv);
+  const bool inf = !GATED && __any_sync(0xffffffffu, isinf(amax));
+  if (!live) return;
+#pragma unroll
+  for (int k = 0; k < P; ++k) {
+    if (inf) no_infinities(v[k]);
+    put8(out, ld, c0 + kStep * k, v[k], inv);
+  }
+  if (to) *to = s;
+}
+
+// The same for any other rows: a half-warp per block, element by element.
+template <bool BF16, bool GATED>
+__global__ void __launch_bounds__(256) quantize_any_kernel(const void* __restrict__ x, uint32_t n_all, int cols,
+                                                          FastDiv kb, int64_t ld, uint8_t* __restrict__ q,
+                                                          float* __restrict__ scales) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int sub = threadIdx.x & (kLanesPerBlock - 1);
+  const uint32_t i = blockIdx.x * 16 + threadIdx.x / kLanesPerBlock;
+  const bool live = i < n_all;
+  const uint32_t row = div_by(i, kb);
+  const int c = (int)(i - row * kb.d) * kFp8Block + sub * kVec;
+  const int n = live ? cols - c : 0;
+  const int64_t at = (int64_t)row * cols * (GATED ? 2 : 1) + c;
+  float v[8];
+  load8<BF16, false>(x, at, n, v);
+  if (GATED) {
+    float u[8];
+    load8<BF16, false>(x, at + cols, n, u);
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const float2 h = swiglu2(make_float2(v[j], v[j + 1]), make_float2(u[j], u[j + 1]));
+      v[j] = h.x;
+      v[j + 1] = h.y;
+    }
+  }
+  const float amax = block_max(absmax8(v));
+  uint8_t* out = live ? q + row * ld : nullptr;
+  float* to = live && sub == 0 ? scales + i : nullptr;
+  if (GATED && __any_sync(0xffffffffu, live && fp8_scale_unsure(amax))) {
+    swiglu64<BF16, false>(x, at, cols, n, out, ld, c, 1, kLanesPerBlock, to);
+    return;
+  }
+  float inv;
+  const float s = fp8_scale(amax, &inv);
+  if (!GATED && __any_sync(0xffffffffu, isinf(amax))) no_infinities(v);
+  if (out) put8(out, ld, c, v, inv);
+  if (to) *to = s;
 }
 
 // A thread's 8 elements as they lie in shared memory (bf16: 16 bytes, fp32: 32).
@@ -726,56 +806,126 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
   }
 }
 
-// One CTA per 128 x 128 block: warp w holds rows w, w + 8, ... (16 of them),
-// lane l the columns 4 l .. 4 l + 3, in registers between the maximum and the
-// output.
-template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(256, 2) encode_kernel(const void* __restrict__ w, int N, int K, int nb, int kb,
-                                                    uint8_t* __restrict__ q, float* __restrict__ scales) {
+// Blocks of 128 x 128, blockIdx.x, + gridDim.x, ... one after another, the next
+// ones on their way into shared memory (cp.async: each thread copies and reads
+// its own pieces, no barrier). Of T threads, thread t has the pieces of 16
+// bytes t, t + T, ... of the block's rows. Rows of whole pieces. 14336 x 3584
+// fp32 takes 48 us (5.3 TB/s), 55 with 512 threads; held in registers from
+// load to store, with two CTAs of 256 threads per SM taking turns, 52.
+// 11008 x 2048 bf16: 16 us against 26.
+template <bool BF16>
+struct Enc {
+  static constexpr int kThreads = BF16 ? 512 : 1024;
+  static constexpr int kPer = BF16 ? 8 : 4;                     // elements of a piece
+  static constexpr int kRow = kFp8Block / kPer;                 // pieces of a row
+  static constexpr int kPieces = kFp8Block * kRow / kThreads;   // of a thread
+  static constexpr int kSlots = BF16 ? 4 : 3;
+  static constexpr int kSlot = kFp8Block * kFp8Block * (BF16 ? 2 : 4);
+};
+template <bool BF16>
+__global__ void __launch_bounds__(Enc<BF16>::kThreads, 1) encode_kernel(const void* __restrict__ w, int N, int K, int nb, int kb,
+                                                    int64_t n_all, uint8_t* __restrict__ q,
+                                                    float* __restrict__ scales) {
+  using E = Enc<BF16>;
+  constexpr int S = E::kSlots, P = E::kPieces, T = E::kThreads, R = T / E::kRow;  // rows between a thread's pieces
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float part[2][32];
+  const int tid = threadIdx.x, c_in = tid % E::kRow * E::kPer, r_in = tid / E::kRow;
   pdl_launch_dependents();
   pdl_wait();
-  const int64_t blk = blockIdx.x;  // (expert, row block, column block)
-  const int b = (int)(blk % kb);
-  const int64_t en = blk / kb;
-  const int rb = (int)(en % nb);
-  const int64_t e = en / nb;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = b * kFp8Block + lane * 4;
-  float v[16][4];
-  float m = 0.f;
+  // (expert, row block, column block) of block i: its first row and column
+  auto place = [&](int64_t i, int64_t& row, int& rows, int& c) {
+    const int64_t en = i / kb;
+    c = (int)(i - en * kb) * kFp8Block + c_in;
+    const int64_t e = en / nb;
+    const int rb = (int)(en - e * nb);
+    row = e * N + rb * kFp8Block;
+    rows = min(kFp8Block, N - rb * kFp8Block);
+  };
+  auto fetch = [&](int64_t i, int slot) {
+    if (i < n_all) {
+      int64_t row;
+      int rows, c;
+      place(i, row, rows, c);
+      const uint8_t* src = static_cast<const uint8_t*>(w) + ((row + r_in) * K + c) * (BF16 ? 2 : 4);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = rb * kFp8Block + i * 8 + warp;
-    const int64_t at = (e * N + r) * (int64_t)K + c;
+      for (int k = 0; k < P; ++k)
+        if (c < K && r_in + k * R < rows)
+          cp_async16(ring + slot * E::kSlot + (k * T + tid) * 16, src + (int64_t)k * R * K * (BF16 ? 2 : 4));
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[i][j] = 0.f;
-    if (r < N) {
-      if (VEC) {
-        if (c < K) {
-          if (BF16) {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + at);
-            v[i][0] = __uint_as_float(u.x << 16);
-            v[i][1] = __uint_as_float(u.x & 0xFFFF0000u);
-            v[i][2] = __uint_as_float(u.y << 16);
-            v[i][3] = __uint_as_float(u.y & 0xFFFF0000u);
-          } else {
-            const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + at);
-            v[i][0] = f.x; v[i][1] = f.y; v[i][2] = f.z; v[i][3] = f.w;
-          }
-        }
-      } else {
+  for (int d = 0; d < S; ++d) fetch(blockIdx.x + (int64_t)d * gridDim.x, d);
+  int slot = 0, flip = 0;
+  for (int64_t i = blockIdx.x; i < n_all; i += gridDim.x, flip ^= 1) {
+    int64_t row;
+    int rows, c;
+    place(i, row, rows, c);
+    asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+    float v[P][E::kPer], m = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (c + j < K)
-            v[i][j] = BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(w)[at + j] << 16)
-                           : static_cast<const float*>(w)[at + j];
+    for (int k = 0; k < P; ++k) {
+      const bool live = c < K && r_in + k * R < rows;
+      const uint4 u = live ? *reinterpret_cast<const uint4*>(ring + slot * E::kSlot + (k * T + tid) * 16)
+                           : make_uint4(0, 0, 0, 0);
+      const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int j = 0; j < E::kPer; ++j) {
+        v[k][j] = __uint_as_float(!BF16 ? x[j % 4] : j & 1 ? x[j / 2] & 0xFFFF0000u : x[j / 2] << 16);
+        m = fmaxf(m, fabsf(v[k][j]));
       }
     }
+    fetch(i + (int64_t)S * gridDim.x, slot);
+    if (++slot == S) slot = 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) part[flip][tid >> 5] = m;
+    __syncthreads();  // (the other half of `part` is written before the next barrier)
+    m = part[flip][tid & (T / 32 - 1)];
+#pragma unroll
+    for (int o = T / 64; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float inv;
+    const float s = fp8_scale(m, &inv);
+    if (tid == 0) scales[i] = s;
+    const bool inf = isinf(m);
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+      if (inf) no_infinities(v[k]);
+      if (c >= K || r_in + k * R >= rows) continue;
+      uint8_t* p = q + (row + r_in + k * R) * K + c;
+      uint32_t b[E::kPer / 4];
+#pragma unroll
+      for (int j = 0; j < E::kPer; j += 4)
+        b[j / 4] = e4m3x4(v[k][j] * inv, v[k][j + 1] * inv, v[k][j + 2] * inv, v[k][j + 3] * inv);
+      if (BF16)
+        *reinterpret_cast<uint2*>(p) = make_uint2(b[0], b[E::kPer / 4 - 1]);
+      else
+        *reinterpret_cast<uint32_t*>(p) = b[0];
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = fmaxf(m, fabsf(v[i][j]));
+}
+
+// The same for any other rows, one CTA per block, element by element: warp w
+// holds rows w, w + 8, ..., lane l the columns l, l + 32, ...
+template <bool BF16>
+__global__ void __launch_bounds__(256) encode_any_kernel(const void* __restrict__ w, int N, int K, int nb, int kb,
+                                                        uint8_t* __restrict__ q, float* __restrict__ scales) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int64_t blk = blockIdx.x, en = blk / kb, e = en / nb;
+  const int c0 = (int)(blk - en * kb) * kFp8Block, rb = (int)(en - e * nb);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto each = [&](auto f) {
+    for (int r = warp; r < min(kFp8Block, N - rb * kFp8Block); r += 8)
+      for (int c = c0 + lane; c < min(c0 + kFp8Block, K); c += 32) {
+        const int64_t at = (e * N + rb * kFp8Block + r) * (int64_t)K + c;
+        f(at, BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(w)[at] << 16)
+                   : static_cast<const float*>(w)[at]);
+      }
+  };
+  float m = 0.f;
+  each([&](int64_t, float v) { m = fmaxf(m, fabsf(v)); });
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   __shared__ float part[8];
@@ -786,23 +936,10 @@ __global__ void __launch_bounds__(256, 2) encode_kernel(const void* __restrict__
   float inv;
   const float s = fp8_scale(m, &inv);
   if (threadIdx.x == 0) scales[blk] = s;
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (isinf(m)) no_infinities(v[i]);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = rb * kFp8Block + i * 8 + warp;
-    if (r >= N) continue;
-    const uint32_t u = e4m3x4(v[i][0] * inv, v[i][1] * inv, v[i][2] * inv, v[i][3] * inv);
-    uint8_t* p = q + (e * N + r) * (int64_t)K + c;
-    if (VEC) {
-      if (c < K) *reinterpret_cast<uint32_t*>(p) = u;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (c + j < K) p[j] = (uint8_t)(u >> (8 * j));
-    }
-  }
+  each([&](int64_t at, float v) {
+    if (isinf(v)) v = fmaf(v, 0.f, v);
+    q[at] = (uint8_t)e4m3x4(v * inv, 0.f, 0.f, 0.f);
+  });
 }
 
 // Weights [N][K] of one expert into the tiles of the handle; one thread per
@@ -833,26 +970,17 @@ __global__ void __launch_bounds__(256) retile_kernel(const uint8_t* __restrict__
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <bool BF16, bool VEC, bool GATED>
-cudaError_t launch_quant_as(const void* x, uint32_t n, int cols, uint8_t* q, float* scales, cudaStream_t s) {
-  const FastDiv kb = fast_div((uint32_t)fp8_blocks(cols));
-  // several blocks per half-warp once that still gives every SM two CTAs
-  constexpr int U = GATED ? 2 : 4;
-  auto go = [&](auto kern, int u) {
-    return launch_pdl(kern, (n + 16 * u - 1) / (16 * u), 256, 0, s, x, n, cols, kb, fp8_ld(cols), q, scales);
-  };
-  if (n >= 300u * 16 * U) return go(quantize_kernel<BF16, VEC, GATED, U>, U);
-  return go(quantize_kernel<BF16, VEC, GATED, 1>, 1);
-}
 template <bool GATED>
 cudaError_t launch_quant(const void* x, int bf16, int64_t rows, int cols, uint8_t* q, float* scales, cudaStream_t s) {
   const uint32_t n = (uint32_t)(rows * fp8_blocks(cols));  // < 2^31, checked by the caller
-  const bool vec = cols % 8 == 0 && aligned16(x);
-  if (bf16)
-    return vec ? launch_quant_as<true, true, GATED>(x, n, cols, q, scales, s)
-               : launch_quant_as<true, false, GATED>(x, n, cols, q, scales, s);
-  return vec ? launch_quant_as<false, true, GATED>(x, n, cols, q, scales, s)
-             : launch_quant_as<false, false, GATED>(x, n, cols, q, scales, s);
+  const FastDiv kb = fast_div((uint32_t)fp8_blocks(cols));
+  constexpr uint32_t kPer = 16 * (GATED ? 2 : 4);  // blocks per CTA
+  auto go = [&](auto kern, uint32_t per) {
+    return launch_pdl(kern, (n + per - 1) / per, 256, 0, s, x, n, cols, kb, fp8_ld(cols), q, scales);
+  };
+  if (cols % 8 == 0 && aligned16(x))
+    return bf16 ? go(quantize_kernel<true, GATED>, kPer) : go(quantize_kernel<false, GATED>, kPer);
+  return bf16 ? go(quantize_any_kernel<true, GATED>, 16) : go(quantize_any_kernel<false, GATED>, 16);
 }
 
 // CTAs of `kern` with t threads and smem bytes of dynamic shared memory that
@@ -939,12 +1067,22 @@ cudaError_t launch_rmsnorm(const NormArgs& a, int x_bf16, int res_bf16, int64_t 
 cudaError_t launch_fp8_encode(const void* w, int bf16, int n_experts, int N, int K, uint8_t* q, float* scales,
                               cudaStream_t s) {
   const int nb = fp8_blocks(N), kb = fp8_blocks(K);
-  const bool vec = K % 8 == 0 && aligned16(w) && (reinterpret_cast<uintptr_t>(q) & 3) == 0;
-  auto go = [&](auto kern) {
-    return launch_pdl(kern, (unsigned)((int64_t)n_experts * nb * kb), 256, 0, s, w, N, K, nb, kb, q, scales);
+  const int64_t n = (int64_t)n_experts * nb * kb;
+  auto go = [&](auto kern, int threads, size_t smem) -> cudaError_t {
+    int64_t fit = 0;
+    const cudaError_t e = resident(reinterpret_cast<const void*>(kern), threads, smem, &fit);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, (unsigned)std::min(n, fit), (unsigned)threads, smem, s, w, N, K, nb, kb, n, q, scales);
   };
-  if (bf16) return vec ? go(encode_kernel<true, true>) : go(encode_kernel<true, false>);
-  return vec ? go(encode_kernel<false, true>) : go(encode_kernel<false, false>);
+  const uintptr_t qa = reinterpret_cast<uintptr_t>(q);
+  if (bf16) {
+    if (K % 8 == 0 && aligned16(w) && qa % 8 == 0)
+      return go(encode_kernel<true>, Enc<true>::kThreads, (size_t)Enc<true>::kSlots * Enc<true>::kSlot);
+    return launch_pdl(encode_any_kernel<true>, (unsigned)n, 256, 0, s, w, N, K, nb, kb, q, scales);
+  }
+  if (K % 4 == 0 && aligned16(w) && qa % 4 == 0)
+    return go(encode_kernel<false>, Enc<false>::kThreads, (size_t)Enc<false>::kSlots * Enc<false>::kSlot);
+  return launch_pdl(encode_any_kernel<false>, (unsigned)n, 256, 0, s, w, N, K, nb, kb, q, scales);
 }
 
 cudaError_t launch_fp8_retile(const uint8_t* src, uint8_t* dst, int N, int K, cudaStream_t s) {
