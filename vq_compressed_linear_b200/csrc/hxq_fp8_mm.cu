@@ -80,9 +80,8 @@ __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
 // The same without ordering any memory but the tensor core's own (the
 // tcgen05 fences do that): a release at cluster scope waits for the thread's
 // stores and costs about a thousand cycles.
-__device__ __forceinline__ void mbar_signal_rank(uint64_t* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];"
-               ::"r"(map_to_rank(smem_u32(bar), rank)) : "memory");
+__device__ __forceinline__ void mbar_signal_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Waits, bounded at kWaitCycles of the SM's clock (about 2 s): false, with
 // *abort set, when the limit passes or another thread of the CTA gave up.
@@ -158,9 +157,9 @@ __device__ __forceinline__ void load_ranges(const Ranges& R, const MmArgs& a) {
   if (GROUPED) {
     const int E = a.n_experts;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
-      const int lo = min(max(__ldg(a.offsets + e), 0), a.M);
+      const int lo = min(max(a.offsets[e], 0), a.M);
       R.first[e] = lo;
-      R.rows[e] = min(max(__ldg(a.offsets + e + 1), lo), a.M) - lo;
+      R.rows[e] = min(max(a.offsets[e + 1], lo), a.M) - lo;
     }
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -422,7 +421,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
     constexpr int NC = BN / 16 / G;  // pieces of 16 columns: piece i is columns 16 (i G + grp) ..
     for (Walk<BN, GROUPED> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
       const int n_out = w.tile * kFp8Block + r;
-      const float bias = a.out.bias && n_out < a.N ? __ldg(a.out.bias + (size_t)w.e * a.N + n_out) : 0.f;
+      const float bias = a.out.bias && n_out < a.N ? a.out.bias[(size_t)w.e * a.N + n_out] : 0.f;
       float acc[NC][16];
 #pragma unroll
       for (int i = 0; i < NC; ++i)
@@ -926,11 +925,10 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
       for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
         const uint32_t idesc = idesc_e4m3(256, w.width);
         for (int kb = 0; kb < a.n_blocks; ++kb) {
+          const uint64_t xd = smem_desc(smem_u32(ring + b * kWideStage)), wd = xd + (kFp8TileBytes >> 4);
           if (!(ok = wait_bar_warp(lane & 1 ? &bar_full[b] : &bar_pfree[p], lane & 1 ? ph : pph ^ 1, abrt))) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint64_t xd = smem_desc(smem_u32(ring + b * kWideStage));
-            const uint64_t wd = xd + (kFp8TileBytes >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) tc_mma2_f8(tmem + p * 256, xd + kk * 2, wd + kk * 2, idesc, kk > 0);
             tc_commit2(&bar_p[p]);
@@ -972,6 +970,7 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWideAddRegs));
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
+    const uint32_t pfree0 = map_to_rank(smem_u32(&bar_pfree[0]), 0);  // in the leading CTA
     int p = 0, sp = 0;
     uint32_t pph = 0, sph = 0;
     bool ok = true;
@@ -997,7 +996,7 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) {
-                mbar_signal_rank(&bar_pfree[p], 0);
+                mbar_signal_at(pfree0 + p * 8);
                 mbar_arrive(&bar_sfree[sp]);
               }
             }
@@ -1018,8 +1017,8 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
         const float* bias = a.out.bias + (size_t)w.e * a.N + n0;
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
-          if (2 * j < n) acc[j].x += __ldg(bias + 2 * j);
-          if (2 * j + 1 < n) acc[j].y += __ldg(bias + 2 * j + 1);
+          if (2 * j < n) acc[j].x += bias[2 * j];
+          if (2 * j + 1 < n) acc[j].y += bias[2 * j + 1];
         }
       }
       uint32_t v[32];

@@ -26,6 +26,8 @@
 namespace hxq {
 namespace {
 
+// (Inputs are read with plain loads, not through the read-only path: the
+// kernels may start while the one that writes their inputs still runs.)
 constexpr int kVec = 8;                        // elements per thread and block of 128: 16 lanes share a block
 constexpr int kLanesPerBlock = kFp8Block / kVec;
 
@@ -236,9 +238,9 @@ __device__ __forceinline__ void unpack(const Raw8<BF16>& r, float (&v)[8]) {
 // gated 30.8 with two (bound by issue slots; fp32 41, 6.4 TB/s) and 37 with
 // four or one.
 template <bool BF16, bool GATED>
-__global__ void __launch_bounds__(256) quantize_kernel(const void* __restrict__ x, uint32_t n_all, int cols, FastDiv kb,
-                                                      int64_t ld, uint8_t* __restrict__ q,
-                                                      float* __restrict__ scales) {
+__global__ void __launch_bounds__(256) quantize_kernel(const void* x, uint32_t n_all, int cols, FastDiv kb,
+                                                      int64_t ld, uint8_t* q,
+                                                      float* scales) {
   constexpr int P = GATED ? 2 : 4, L = kLanesPerBlock / P, kStep = L * kVec;  // pieces, threads of a block
   pdl_launch_dependents();
   pdl_wait();
@@ -293,9 +295,9 @@ __global__ void __launch_bounds__(256) quantize_kernel(const void* __restrict__ 
 
 // The same for any other rows: a half-warp per block, element by element.
 template <bool BF16, bool GATED>
-__global__ void __launch_bounds__(256) quantize_any_kernel(const void* __restrict__ x, uint32_t n_all, int cols,
-                                                          FastDiv kb, int64_t ld, uint8_t* __restrict__ q,
-                                                          float* __restrict__ scales) {
+__global__ void __launch_bounds__(256) quantize_any_kernel(const void* x, uint32_t n_all, int cols,
+                                                          FastDiv kb, int64_t ld, uint8_t* q,
+                                                          float* scales) {
   pdl_launch_dependents();
   pdl_wait();
   const int sub = threadIdx.x & (kLanesPerBlock - 1);
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
             uint4 w;
             load_sum(xslot(d, k), rslot(d, k), a.res, v, w);
             for (int j = 0; j < 8; ++j)
-              if (v[j] != 0.f && (!a.weight || __ldg(a.weight + c0 + kStep * k + j) != 0.f)) any = 1.f;
+              if (v[j] != 0.f && (!a.weight || a.weight[c0 + kStep * k + j] != 0.f)) any = 1.f;
           }
         // (a block's threads are here together; each looks at its own pieces)
         const uint32_t peers = ((1u << L) - 1) << (tid & 31 & ~(L - 1));
@@ -766,7 +768,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
             if (c < cols) load_sum(xslot(d, k), rslot(d, k), a.res, v, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const double e = (double)v[j] * r * (a.weight && c < cols ? (double)__ldg(a.weight + c + j) : 1.0);
+              const double e = (double)v[j] * r * (a.weight && c < cols ? (double)a.weight[c + j] : 1.0);
               m = fmax(m, fabs(e));
               v[j] = (float)e;
             }
@@ -823,9 +825,9 @@ struct Enc {
   static constexpr int kSlot = kFp8Block * kFp8Block * (BF16 ? 2 : 4);
 };
 template <bool BF16>
-__global__ void __launch_bounds__(Enc<BF16>::kThreads, 1) encode_kernel(const void* __restrict__ w, int N, int K, int nb, int kb,
-                                                    int64_t n_all, uint8_t* __restrict__ q,
-                                                    float* __restrict__ scales) {
+__global__ void __launch_bounds__(Enc<BF16>::kThreads, 1) encode_kernel(const void* w, int N, int K, int nb, int kb,
+                                                    int64_t n_all, uint8_t* q,
+                                                    float* scales) {
   using E = Enc<BF16>;
   constexpr int S = E::kSlots, P = E::kPieces, T = E::kThreads, R = T / E::kRow;  // rows between a thread's pieces
   extern __shared__ __align__(16) uint8_t ring[];
@@ -909,8 +911,8 @@ __global__ void __launch_bounds__(Enc<BF16>::kThreads, 1) encode_kernel(const vo
 // The same for any other rows, one CTA per block, element by element: warp w
 // holds rows w, w + 8, ..., lane l the columns l, l + 32, ...
 template <bool BF16>
-__global__ void __launch_bounds__(256) encode_any_kernel(const void* __restrict__ w, int N, int K, int nb, int kb,
-                                                        uint8_t* __restrict__ q, float* __restrict__ scales) {
+__global__ void __launch_bounds__(256) encode_any_kernel(const void* w, int N, int K, int nb, int kb,
+                                                        uint8_t* q, float* scales) {
   pdl_launch_dependents();
   pdl_wait();
   const int64_t blk = blockIdx.x, en = blk / kb, e = en / nb;
