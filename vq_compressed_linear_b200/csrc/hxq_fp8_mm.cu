@@ -649,7 +649,8 @@ cudaError_t launch_skinny(const hxq_fp8& h, const uint8_t* xq, const MmArgs& a, 
 // features, 64 columns at a time, and hand it back before they add the last
 // ones. A block of K takes 775 cycles against the MMAs' 512: the way round a
 // buffer (MMA, commit, read, arrival in the leading CTA, issue) takes 1550.
-// 2048 x 14336 x 3584 runs in 111 us, 1.9 PFLOP/s. Tried and slower there:
+// 2048 x 14336 x 3584 runs in 107 us, 1.96 PFLOP/s. Tried and slower there (at
+// 113 us):
 // halves of 128 features with an MMA and buffers of their own, 126 us (their
 // MMAs read the 256 tokens from shared memory twice); 16 adding warps, 127;
 // reads of 32 columns, each under way while the last one is added, 122.
