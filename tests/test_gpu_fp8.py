@@ -315,7 +315,8 @@ def test_rmsnorm_scales_at_their_borders(hxq, xt, K):
 
 
 def test_other_layouts_are_copied(hxq):
-    """A transposed and a sliced input give what their contiguous copies give; with a stream they are refused."""
+    """A transposed and a sliced input give what their contiguous copies give, on the current stream and on another,
+    by object and by handle, whose work before the call the copy waits for."""
     import torch
     base = randn(3, 200, 300)
     st = torch.cuda.Stream()
@@ -323,8 +324,15 @@ def test_other_layouts_are_copied(hxq):
         for f in (hxq.fp8_quantize, hxq.fp8_encode, lambda v, **k: hxq.rmsnorm(v, **k)[:2]):
             a, b = f(x), f(x.contiguous())
             assert torch.equal(codes_t(a[0]), codes_t(b[0])) and torch.equal(a[1], b[1])
-            with pytest.raises(hxq.HXQError):
-                f(x, stream=st)
+            keep = base.clone()
+            for handle in (st, st.cuda_stream):
+                base.zero_()
+                st.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.stream(st):
+                    base.copy_(keep)
+                c = f(x, stream=handle)
+                st.synchronize()
+                assert torch.equal(codes_t(a[0]), codes_t(c[0])) and torch.equal(a[1], c[1])
 
 
 def test_row_operators_on_another_stream_and_captured(hxq):

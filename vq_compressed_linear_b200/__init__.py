@@ -452,7 +452,8 @@ def encode(W, mode, codebook, threshold, max_sidecar=None, stream=None):
 
 # ---- 8-bit-float layers --------------------------------------------------------
 # Tensors are checked here for what the C ABI cannot see: shape, type,
-# contiguity and device. A mismatch raises HXQError with HXQ_EINVAL. These
+# contiguity and device. A mismatch raises HXQError with HXQ_EINVAL. A call
+# runs on the current torch stream, or on `stream` as if it were that. These
 # wrappers sit in the path of a decode step: they call the library directly,
 # take outputs that exist already, and build no message unless they raise.
 
@@ -486,22 +487,20 @@ def _refuse(what: str):
     raise HXQError(HXQ_EINVAL, what)
 
 
-def _raw(stream, device: int):
-    return _torch.raw_stream(device) if stream is None else int(getattr(stream, "cuda_stream", stream))
+def _on(stream):
+    """`stream` (a Stream, or its handle) as the current one: what a wrapper
+    copies or allocates then belongs to the stream that its kernel runs on."""
+    import torch
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
 
 
-def _input(t, dims: int, stream, what: str):
-    """`t` contiguous and its HXQ_TYPE_*: float32 or bfloat16 on the current
-    CUDA device. Other layouts are copied, on the current stream: with a
-    stream given they are refused, since nothing would order the two."""
+def _input(t, dims: int, what: str):
+    """`t` contiguous (other layouts are copied) and its HXQ_TYPE_*: float32
+    or bfloat16 on the current CUDA device."""
     code = _t().code.get(t.dtype)
     if code is None or not t.is_cuda or t.dim() != dims or t.get_device() != _torch.device():
         _refuse(f"{what}: a {dims}D float32 or bfloat16 tensor on the current CUDA device")
-    if t.is_contiguous():
-        return t, code
-    if stream is not None:
-        _refuse(f"{what}: a contiguous tensor, where a stream is given")
-    return t.contiguous(), code
+    return (t if t.is_contiguous() else t.contiguous()), code
 
 
 def _output(t, shape, dtype, device: int, what: str):
@@ -523,11 +522,14 @@ def _bytes(t, shape, device: int, what: str):
 def fp8_quantize(x, q=None, scales=None, stream=None):
     """x [M, K] (float32 or bfloat16 CUDA) as an 8-bit activation. Returns
     (q float8_e4m3fn [M, K rounded up to 16], scales float32 [M, ceil(K / 128)])."""
-    x, code = _input(x, 2, stream, "fp8_quantize")
+    if stream is not None:
+        with _on(stream):
+            return fp8_quantize(x, q, scales)
+    x, code = _input(x, 2, "fp8_quantize")
     (rows, cols), dev = x.shape, x.get_device()
     q = _bytes(q, (rows, (cols + 15) // 16 * 16), dev, "fp8_quantize: q")
     scales = _output(scales, (rows, (cols + 127) // 128), _torch.f32, dev, "fp8_quantize: scales")
-    _check(lib.hxq_fp8_quantize(x.data_ptr(), code, rows, cols, q.data_ptr(), scales.data_ptr(), _raw(stream, dev)),
+    _check(lib.hxq_fp8_quantize(x.data_ptr(), code, rows, cols, q.data_ptr(), scales.data_ptr(), _torch.raw_stream(dev)),
            "hxq_fp8_quantize")
     return q, scales
 
@@ -535,14 +537,17 @@ def fp8_quantize(x, q=None, scales=None, stream=None):
 def fp8_swiglu(gate_up, q=None, scales=None, stream=None):
     """silu(gate) * up of gate_up [M, 2 K] (gate first) as an 8-bit
     activation [M, K]; returns (q, scales) as fp8_quantize."""
-    x, code = _input(gate_up, 2, stream, "fp8_swiglu")
+    if stream is not None:
+        with _on(stream):
+            return fp8_swiglu(gate_up, q, scales)
+    x, code = _input(gate_up, 2, "fp8_swiglu")
     (rows, both), dev = x.shape, x.get_device()
     if both % 2:
         _refuse("fp8_swiglu: gate_up is [M, 2 K]")
     cols = both // 2
     q = _bytes(q, (rows, (cols + 15) // 16 * 16), dev, "fp8_swiglu: q")
     scales = _output(scales, (rows, (cols + 127) // 128), _torch.f32, dev, "fp8_swiglu: scales")
-    _check(lib.hxq_fp8_swiglu(x.data_ptr(), code, rows, cols, q.data_ptr(), scales.data_ptr(), _raw(stream, dev)),
+    _check(lib.hxq_fp8_swiglu(x.data_ptr(), code, rows, cols, q.data_ptr(), scales.data_ptr(), _torch.raw_stream(dev)),
            "hxq_fp8_swiglu")
     return q, scales
 
@@ -551,12 +556,15 @@ def fp8_encode(W, q=None, scales=None, stream=None):
     """Weights [N, K] or [E, N, K] (float32 or bfloat16 CUDA) as 8-bit values
     of the same shape and scales [(E,) ceil(N / 128), ceil(K / 128)]: what
     Fp8Linear takes."""
-    W, code = _input(W, 3 if W.dim() == 3 else 2, stream, "fp8_encode")
+    if stream is not None:
+        with _on(stream):
+            return fp8_encode(W, q, scales)
+    W, code = _input(W, 3 if W.dim() == 3 else 2, "fp8_encode")
     dev, (N, K) = W.get_device(), W.shape[-2:]
     q = _bytes(q, W.shape, dev, "fp8_encode: q")
     scales = _output(scales, (*W.shape[:-2], (N + 127) // 128, (K + 127) // 128), _torch.f32, dev, "fp8_encode: scales")
     _check(lib.hxq_fp8_encode(W.data_ptr(), code, W.shape[0] if W.dim() == 3 else 1, N, K, q.data_ptr(),
-                              scales.data_ptr(), _raw(stream, dev)), "hxq_fp8_encode")
+                              scales.data_ptr(), _torch.raw_stream(dev)), "hxq_fp8_encode")
     return q, scales
 
 
@@ -570,7 +578,10 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=Non
     given of y and q (q if neither is). sum_out receives t (it may be the
     residual itself; a new tensor if there is a residual and none is given).
     Returns (q, scales, y, sum), None for what was not asked for."""
-    x, xt = _input(x, 2, stream, "rmsnorm")
+    if stream is not None:
+        with _on(stream):
+            return rmsnorm(x, weight, eps, residual, sum_out, y, q, scales, want)
+    x, xt = _input(x, 2, "rmsnorm")
     rt = xt
     T = _torch
     shape, dev = x.shape, x.get_device()
@@ -585,7 +596,7 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=Non
     if residual is not None:
         if residual.dtype is not x.dtype or residual.shape != shape or not residual.is_contiguous() or \
                 residual.get_device() != dev:  # (not the common case)
-            residual, rt = _input(residual, 2, stream, "rmsnorm: residual")
+            residual, rt = _input(residual, 2, "rmsnorm: residual")
             if residual.shape != shape:
                 _refuse("rmsnorm: residual has the shape of x")
         sum_out = _output(sum_out, shape, residual.dtype, dev, "rmsnorm: sum_out")
@@ -604,7 +615,7 @@ def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=Non
         y = _output(y, shape, T.bf16, dev, "rmsnorm: y")
         yp = y.data_ptr()
     rc = lib.hxq_rmsnorm(x.data_ptr(), xt, rp, sp, rt, wp, eps, rows, cols, yp, qp, cp,
-                         T.raw_stream(dev) if stream is None else _raw(stream, dev))
+                         T.raw_stream(dev))
     if rc:
         raise HXQError(rc, "hxq_rmsnorm")
     return q, scales, y, sum_out
@@ -635,7 +646,7 @@ class Fp8Linear:
         """From float32 or bfloat16 CUDA weights [N, K] or [E, N, K]."""
         return cls(*fp8_encode(W))
 
-    def _args(self, xq, xs, bias, out_dtype, y, stream):
+    def _args(self, xq, xs, bias, out_dtype, y):
         T = _torch
         M, dev = xq.shape[0], xq.get_device()
         if dev != self._dev:
@@ -646,14 +657,17 @@ class Fp8Linear:
         if bias is not None:
             bp = _output(bias, (self.E, self.N) if self.grouped else (self.N,), T.f32, dev, "Fp8Linear: bias").data_ptr()
         y = _output(y, (M, self.N), T.bf16 if out_dtype == HXQ_OUT_BF16 else T.f32, dev, "Fp8Linear: y")
-        return M, xq.data_ptr(), xs.data_ptr(), bp, y, _raw(stream, dev)
+        return M, xq.data_ptr(), xs.data_ptr(), bp, y, T.raw_stream(dev)
 
     def forward(self, xq, xs, bias=None, out_dtype=HXQ_OUT_F32, y=None, stream=None):
         """y = x . W^T (+ bias [N]) as float32, or as bfloat16 with
         out_dtype=HXQ_OUT_BF16."""
+        if stream is not None:
+            with _on(stream):
+                return self.forward(xq, xs, bias, out_dtype, y)
         if self.grouped:
             _refuse("Fp8Linear: forward_grouped runs the experts")
-        M, xp, sp, bp, y, st = self._args(xq, xs, bias, out_dtype, y, stream)
+        M, xp, sp, bp, y, st = self._args(xq, xs, bias, out_dtype, y)
         _check(lib.hxq_fp8_forward(self.handle, xp, sp, bp, y.data_ptr(), out_dtype, M, st), "hxq_fp8_forward")
         return y
 
@@ -663,9 +677,12 @@ class Fp8Linear:
         """Rows offsets[e] .. offsets[e + 1] - 1 (int32 CUDA [E + 1]) times
         expert e's weights (+ bias [E, N]). Rows outside all of them are left
         as they were in y (unwritten in a new y)."""
+        if stream is not None:
+            with _on(stream):
+                return self.forward_grouped(xq, xs, offsets, bias, out_dtype, y)
         if not self.grouped or offsets is None:
             _refuse("Fp8Linear: forward_grouped takes weights [E, N, K] and offsets")
-        M, xp, sp, bp, y, st = self._args(xq, xs, bias, out_dtype, y, stream)
+        M, xp, sp, bp, y, st = self._args(xq, xs, bias, out_dtype, y)
         op = _output(offsets, (self.E + 1,), _torch.i32, xq.get_device(), "Fp8Linear: offsets").data_ptr()
         _check(lib.hxq_fp8_forward_grouped(self.handle, xp, sp, op, bp, y.data_ptr(), out_dtype, M, st),
                "hxq_fp8_forward_grouped")
