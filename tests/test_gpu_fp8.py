@@ -628,6 +628,64 @@ def test_two_streams_on_one_handle(hxq):
     lin.check()
 
 
+def test_two_graphs_of_one_handle_at_once(hxq):
+    """Graphs captured from the same handles, replayed over one another on two streams."""
+    import torch
+    wq, ws = make_weights(3, 4, 1024, 1152)
+    lin, ex = hxq.Fp8Linear(wq[0], ws[0]), hxq.Fp8Linear(wq, ws)
+    graphs = []
+    for i, m in enumerate((5, 40)):
+        q, s = make_activation(i, m, 1152)
+        Q, S = make_activation(10 + i, 20 * m, 1152)
+        off = offsets_of([3 * m, 0, 16 * m, m])
+        want = [lin.forward(q, s), lin.forward(Q, S), ex.forward_grouped(Q, S, off)]
+        st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=st):
+            got = [lin.forward(q, s), lin.forward(Q, S), ex.forward_grouped(Q, S, off)]
+        graphs.append((g, st, want, got, (q, s, Q, S, off)))  # (the graph's inputs stay alive)
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for g, st, *_ in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for _, _, want, got, _ in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    ex.check()
+
+
+def test_host_threads(hxq):
+    """Calls from several host threads, each on a stream of its own."""
+    import threading
+    import torch
+    wq, ws = make_weights(3, 1, 640, 512)
+    lin = hxq.Fp8Linear(wq[0], ws[0])
+    x = randn(1, 70, 512)
+    want = lin.forward(*hxq.fp8_quantize(x))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(50):
+                    y = lin.forward(*hxq.fp8_quantize(x))
+                st.synchronize()
+            if not torch.equal(y, want):
+                bad.append("differs")
+        except Exception as e:  # noqa: BLE001
+            bad.append(repr(e))
+
+    ts = [threading.Thread(target=work) for _ in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad, bad
+
+
 def mlp(hxq, x, res, w, gate_up, down, bufs):
     """norm -> gate|up -> gated activation -> down, every output in a buffer of its own."""
     q, s, _, t = hxq.rmsnorm(x, w, 1e-6, residual=res, sum_out=bufs["sum"], q=bufs["q"], scales=bufs["s"])
