@@ -199,6 +199,26 @@ def test_swiglu_extremes(hxq):
     check_bytes(q, s, h, 256, DELTA)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [256, 250])
+def test_swiglu_low_gates_large_ups(hxq, dt, K):
+    """Gates at and below -87, where e^-g nears the end of fp32, beside ups that keep the value large."""
+    import torch
+    gu = randn(3, 6, 2 * K)
+    gu[0, :K] = -torch.linspace(80, 95, K).cuda()
+    gu[0, K:] = 3e38
+    gu[1, 5], gu[1, K + 5] = -88.0, 3e38
+    gu[2, 6], gu[2, K + 6] = -300.0, -3e38
+    gu[3, :K] = -88.5
+    gu[4, 9], gu[4, K + 9] = -87.0, 3e38
+    gu[5, 9], gu[5, K + 9] = -104.0, -3e38
+    gu = gu.to(dtype(dt))
+    g, u = f64(gu[:, :K]), f64(gu[:, K:])
+    h = g / (1 + np.exp(-g)) * u
+    q, s = hxq.fp8_swiglu(gu)
+    check_bytes(q, s, h, K, DELTA)
+
+
 # ---- norm -------------------------------------------------------------------------
 
 def ref_norm(x, res, w, eps):
