@@ -219,6 +219,31 @@ def test_swiglu_low_gates_large_ups(hxq, dt, K):
     check_bytes(q, s, h, K, DELTA)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [256, 250])
+def test_swiglu_ends_of_range(hxq, dt, K):
+    """Gates near fp32's largest, infinite and below its normal numbers, beside small and large ups."""
+    import torch
+    inf = float("inf")
+    gu = randn(4, 8, 2 * K)
+    gu[0, 5], gu[0, K + 5] = 3e38, 1e-38
+    gu[1, 5], gu[1, K + 5] = 3e38, 1.0
+    gu[2, 5], gu[2, K + 5] = 3e38, 3e38
+    gu[3, 5], gu[3, K + 5] = inf, -1.0
+    gu[4, 5], gu[4, K + 5] = -inf, 1.0
+    gu[5, :K], gu[5, K:] = 3 * 2.0 ** -133, 2.0 ** 127
+    gu[5, 5], gu[5, K + 5] = 1.0, 2.0 ** -6
+    gu[6, 5], gu[6, K + 5] = 1.0, inf
+    gu[7, 5], gu[7, K + 5] = -60.0, 3e38
+    gu = gu.to(dtype(dt))
+    g, u = f64(gu[:, :K]), f64(gu[:, K:])
+    with np.errstate(over="ignore", invalid="ignore"):
+        h = g / (1 + np.exp(-g)) * u
+    h[np.abs(h) > np.finfo(np.float32).max] = inf  # beyond fp32 it counts as infinite
+    q, s = hxq.fp8_swiglu(gu)
+    check_bytes(q, s, h, K, DELTA)
+
+
 # ---- norm -------------------------------------------------------------------------
 
 def ref_norm(x, res, w, eps):

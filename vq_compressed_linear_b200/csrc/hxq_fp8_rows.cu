@@ -141,10 +141,12 @@ __device__ __forceinline__ void put8(uint8_t* row, int64_t ld, int c, const floa
 // silu(g) * u of two elements. e^-g = 2^p (1 + r ln 2) with p = -g log2(e)
 // rounded and r what the rounding left (exact by FMA, plus the constant's own
 // tail): 2^p is the hardware's (2 ulp), the reciprocal too (1 ulp), and four
-// more roundings follow. For g >= kGateMin: below, e^-g nears the end of fp32,
-// which an up near that end makes large again, so the block is formed in 64
-// bits.
-constexpr float kGateMin = -87.f;
+// more roundings follow. For kGateMin <= g <= kGateMax: below, e^-g nears the end
+// of fp32, which an up near that end makes large again; above, p leaves fp32. A
+// block with such a gate is formed in 64 bits. g u comes first: what it loses
+// below fp32's normal numbers is far below any block's maximum that is not
+// formed in 64 bits, and beyond fp32's end it makes that maximum infinite.
+constexpr float kGateMin = -87.f, kGateMax = 1e38f;
 __device__ __forceinline__ float2 swiglu2(float2 g, float2 u) {
   constexpr float kLog2e = 1.44269504f;                                    // log2(e) to fp32,
   constexpr float kLog2eTail = (float)(1.4426950408889634 - 1.44269504f);  // and the rest
@@ -158,12 +160,12 @@ __device__ __forceinline__ float2 swiglu2(float2 g, float2 u) {
   const float2 d = __fadd2_rn(e, make_float2(1.f, 1.f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv.y) : "f"(d.y));
-  return __fmul2_rn(__fmul2_rn(g, inv), u);
+  return __fmul2_rn(__fmul2_rn(g, u), inv);
 }
 // One thread's part of a block (8 columns from c0 + 8 lanes k on for each of
 // its `pieces`, `lanes` threads a block) formed in 64 bits, for blocks whose scale
-// fp32 cannot settle or with a gate below kGateMin (a call: its registers are not the fast path's). at: the
-// gate of column c0; n: columns from c0 on.
+// fp32 cannot settle or with a gate outside swiglu2's range (a call: its registers
+// are not the fast path's). at: the gate of column c0; n: columns from c0 on.
 template <bool BF16, bool VEC>
 __device__ __noinline__ void swiglu64(const void* x, int64_t at, int cols, int n, uint8_t* row, int64_t ld, int c0,
                                       int pieces, int lanes, float* scale) {
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const void* x, uint32_t n
     ra[k] = load_raw<BF16>(x, at + kStep * k, kStep * k < n);
     if (GATED) rb[k] = load_raw<BF16>(x, at + cols + kStep * k, kStep * k < n);
   }
-  float v[P][8], amax = 0.f, gmin = 0.f;
+  float v[P][8], amax = 0.f, gmin = 0.f, gmax = 0.f;
 #pragma unroll
   for (int k = 0; k < P; ++k) {
     unpack<BF16>(ra[k], v[k]);
@@ -266,6 +268,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const void* x, uint32_t n
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         gmin = fminf(gmin, fminf(v[k][j], v[k][j + 1]));
+        gmax = fmaxf(gmax, fmaxf(v[k][j], v[k][j + 1]));
         const float2 h = swiglu2(make_float2(v[k][j], v[k][j + 1]), make_float2(u[j], u[j + 1]));
         v[k][j] = h.x;
         v[k][j + 1] = h.y;
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(256) quantize_kernel(const void* x, uint32_t n
   for (int o = 1; o < L; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   uint8_t* out = live ? q + row * ld : nullptr;
   float* to = live && threadIdx.x % L == 0 ? scales + i : nullptr;
-  if (GATED && __any_sync(0xffffffffu, live && (gmin < kGateMin || fp8_scale_unsure(amax)))) {
+  if (GATED && __any_sync(0xffffffffu, live && (gmin < kGateMin || gmax > kGateMax || fp8_scale_unsure(amax)))) {
     swiglu64<BF16, true>(x, at, cols, n, out, ld, c0, P, L, to);
     return;
   }
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(256) quantize_any_kernel(const void* x, uint32
   const int c = (int)(i - row * kb.d) * kFp8Block + sub * kVec;
   const int n = live ? cols - c : 0;
   const int64_t at = (int64_t)row * cols * (GATED ? 2 : 1) + c;
-  float v[8], gmin = 0.f;
+  float v[8], gmin = 0.f, gmax = 0.f;
   load8<BF16, false>(x, at, n, v);
   if (GATED) {
     float u[8];
@@ -315,6 +318,7 @@ __global__ void __launch_bounds__(256) quantize_any_kernel(const void* x, uint32
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       gmin = fminf(gmin, fminf(v[j], v[j + 1]));
+      gmax = fmaxf(gmax, fmaxf(v[j], v[j + 1]));
       const float2 h = swiglu2(make_float2(v[j], v[j + 1]), make_float2(u[j], u[j + 1]));
       v[j] = h.x;
       v[j + 1] = h.y;
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(256) quantize_any_kernel(const void* x, uint32
   const float amax = block_max(absmax8(v));
   uint8_t* out = live ? q + row * ld : nullptr;
   float* to = live && sub == 0 ? scales + i : nullptr;
-  if (GATED && __any_sync(0xffffffffu, live && (gmin < kGateMin || fp8_scale_unsure(amax)))) {
+  if (GATED && __any_sync(0xffffffffu, live && (gmin < kGateMin || gmax > kGateMax || fp8_scale_unsure(amax)))) {
     swiglu64<BF16, false>(x, at, cols, n, out, ld, c, 1, kLanesPerBlock, to);
     return;
   }
