@@ -520,6 +520,22 @@ def test_extreme_scales(hxq):
     assert torch.equal(y, hxq.Fp8Linear(wq[0], ws[0]).forward(xq, xs))
 
 
+@pytest.mark.parametrize("M", [1, 24, 60, 500])
+@pytest.mark.parametrize("e", [-112, 112])
+def test_scales_at_the_ends_of_fp32(hxq, M, e):
+    """Products times one scale alone would over- or underflow; times both they are ordinary."""
+    import torch
+    xq, xs = make_activation(1, M, 640)
+    wq, ws = make_weights(2, 1, 200, 640)
+    # (powers of two near 1, so that none of the scales itself leaves fp32)
+    xs = 2.0 ** torch.randint(-2, 3, xs.shape, device="cuda").float()
+    ws = 2.0 ** torch.randint(-2, 3, ws.shape, device="cuda").float()
+    want = hxq.Fp8Linear(wq[0], ws[0]).forward(xq, xs)
+    assert torch.isfinite(want).all() and want.abs().max() > 2.0 ** 16
+    y = hxq.Fp8Linear(wq[0], ws[0] * 2.0 ** -e).forward(xq, xs * 2.0 ** e)
+    assert torch.equal(y, want)
+
+
 def offsets_of(counts, first=0):
     import torch
     return torch.tensor(np.concatenate([[first], first + np.cumsum(counts)]), dtype=torch.int32, device="cuda")

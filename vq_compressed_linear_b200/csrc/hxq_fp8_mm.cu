@@ -452,7 +452,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
               if (lane == 0) mbar_arrive(&bar_pfree[p]);
             }
             const float* s = sc[sp][k];
-            const float ws = s[BN];
+            const float ws = s[BN];  // (times the token's first: P times one scale alone may leave fp32)
 #pragma unroll
             for (int i = 0; i < NC; ++i)
               if (live(i)) {
@@ -460,10 +460,10 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                   const float4 s4 = *reinterpret_cast<const float4*>(s + 16 * (i * G + grp) + j);
-                  acc[i][j] = fmaf(__uint_as_float(v[j]) * s4.x, ws, acc[i][j]);
-                  acc[i][j + 1] = fmaf(__uint_as_float(v[j + 1]) * s4.y, ws, acc[i][j + 1]);
-                  acc[i][j + 2] = fmaf(__uint_as_float(v[j + 2]) * s4.z, ws, acc[i][j + 2]);
-                  acc[i][j + 3] = fmaf(__uint_as_float(v[j + 3]) * s4.w, ws, acc[i][j + 3]);
+                  acc[i][j] = fmaf(__uint_as_float(v[j]), s4.x * ws, acc[i][j]);
+                  acc[i][j + 1] = fmaf(__uint_as_float(v[j + 1]), s4.y * ws, acc[i][j + 1]);
+                  acc[i][j + 2] = fmaf(__uint_as_float(v[j + 2]), s4.z * ws, acc[i][j + 2]);
+                  acc[i][j + 3] = fmaf(__uint_as_float(v[j + 3]), s4.w * ws, acc[i][j + 3]);
                 }
               }
           }
