@@ -426,7 +426,8 @@ int hxq_fp8_quantize(const void* x, int x_type, int64_t rows, int cols, uint8_t*
  * The gated activation between an MLP's products, as an 8-bit activation:
  * gate_up [rows][2 * cols] holds gate in its first cols columns and up in the
  * others; q and scales [rows][cols] receive gate / (1 + exp(-gate)) * up,
- * formed in fp32. Errors as hxq_fp8_quantize.
+ * formed in fp32 (a value beyond its range counts as infinite). Errors as
+ * hxq_fp8_quantize.
  */
 int hxq_fp8_swiglu(const void* gate_up, int type, int64_t rows, int cols, uint8_t* q, float* scales,
                    void* stream);

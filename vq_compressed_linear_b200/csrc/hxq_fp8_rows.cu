@@ -236,7 +236,7 @@ __device__ __forceinline__ void unpack(const Raw8<BF16>& r, float (&v)[8]) {
 // 16-byte pieces. More pieces pay less often for what is done once per block
 // and thread (shuffles, scale, addresses), and hold more registers: plain
 // 2048 x 14336 bf16 takes 14.1 us with four (6.3 TB/s) and 17.6 with one,
-// gated 30.8 with two (bound by issue slots; fp32 41, 6.4 TB/s) and 37 with
+// gated 31.2 with two (bound by issue slots; fp32 41, 6.4 TB/s) and 37 with
 // four or one.
 template <bool BF16, bool GATED>
 __global__ void __launch_bounds__(256) quantize_kernel(const void* x, uint32_t n_all, int cols, FastDiv kb,
