@@ -493,8 +493,8 @@ int hxq_fp8_create(const uint8_t* W, const float* scales, int n_experts, int N, 
  * value before the output's rounding. Results are bitwise repeatable; a row's result does not
  * depend on the other rows' values.
  * Returns HXQ_EINVAL for a NULL handle/xq/xs/y, a handle of several experts,
- * M < 0, an unknown out_type, misaligned pointers, 2^31 output tiles, or
- * another device current; HXQ_ECUDA if a launch fails.
+ * M < 0 or above 2^31 - 256, an unknown out_type, misaligned pointers, 2^31
+ * output tiles, or another device current; HXQ_ECUDA if a launch fails.
  */
 int hxq_fp8_forward(hxq_fp8_t h, const uint8_t* xq, const float* xs, const float* bias, void* y, int out_type,
                     int M, void* stream);

@@ -1,5 +1,6 @@
 // C ABI of the 8-bit-float layers: argument checks, the weight handle and
 // kernel dispatch.
+#include <climits>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -67,8 +68,8 @@ int mm_impl(hxq_fp8_t h, const uint8_t* xq, const float* xs, const int32_t* offs
   if (!aligned(xq, 16) || !aligned(xs, 4) || !aligned(offsets, 4) || !aligned(bias, 4) ||
       !aligned(y, out_type == HXQ_TYPE_BF16 ? 2 : 4))
     return HXQ_EINVAL;
-  // (row tile, weight tile) units are numbered in 32 bits
-  if (((int64_t)M + h->n_experts) * h->n_tiles >= kMaxBlocks) return HXQ_EINVAL;
+  // rows are counted up to whole blocks of 256, and (row tile, weight tile) units numbered, in 32 bits
+  if (M > INT_MAX - 255 || ((int64_t)M + h->n_experts) * h->n_tiles >= kMaxBlocks) return HXQ_EINVAL;
   if (const int rc = check_current(h->device)) return rc;
   const hxq::Fp8Out out{y, bias, out_type == HXQ_TYPE_BF16 ? 1 : 0};
   return fp8_status(hxq::launch_fp8_mm(*h, xq, xs, offsets, out, M, static_cast<cudaStream_t>(stream)));
