@@ -1,0 +1,30 @@
+"""The 8-bit-float kernels beyond their first pieces: persistent loops that come round, rings that are filled
+again, pieces and pairs that end early. Forms and tolerances are those of test_gpu_fp8."""
+import pytest
+
+from test_gpu_fp8 import (check_product, dense_w, dense_x, make_activation, make_weights, offsets_of)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("out", [0, 1])
+def test_pairs_with_one_empty_half(hxq, out):
+    """Blocks of 256 tokens of which at most 128 exist: the second CTA of a pair stores nothing and comes to the end
+    with its last arrivals in the first one just sent. Launches follow one another at once; every one gives the same
+    bits, and no wait runs out."""
+    import torch
+    E, N, K, n = 40, 1024, 512, 120
+    xq, xs = make_activation(1, E * n, K)
+    wq, ws = make_weights(2, E, N, K)
+    off = offsets_of([n] * E)
+    lin = hxq.Fp8Linear(wq, ws)
+    ys = [lin.forward_grouped(xq, xs, off, out_dtype=out) for _ in range(60)]
+    one = hxq.Fp8Linear(wq[0], ws[0])
+    zs = [one.forward(xq[:1400], xs[:1400], out_dtype=out) for _ in range(60)]  # (5 blocks and 120 rows)
+    lin.check()
+    one.check()
+    assert all(torch.equal(y, ys[0]) for y in ys) and all(torch.equal(z, zs[0]) for z in zs)
+    for e in range(E):
+        r = slice(e * n, (e + 1) * n)
+        check_product(ys[0][r], dense_x(xq[r], xs[r], K), dense_w(wq[e], ws[e]), None, f"expert {e}")
+    check_product(zs[0], dense_x(xq[:1400], xs[:1400], K), dense_w(wq[0], ws[0]), None)

@@ -915,12 +915,16 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
           if (++b == S) b = 0, ph ^= 1;
         }
       }
+      // The leading CTA's tensor core arrives on this CTA's bar_empty after bar_p, which the adders wait for: the last
+      // stages' arrivals land before the CTA leaves its shared memory.
+      for (int i = max(0, issued - S); ok && i < issued; ++i)
+        ok = wait_bar_warp(&bar_empty[i % S], (i / S) & 1, abrt);
       if (*abrt && rank == 0) {  // let the copies land before the CTA ends (the other CTA's are counted here too)
         volatile int never = 0;
         for (int i = max(0, issued - S); i < issued; ++i) wait_bar(&bar_full[i % S], (i / S) & 1, &never);
       }
     } else if (warp == 1 && rank == 0) {
-      int b = 0, p = 0;
+      int b = 0, p = 0, issued = 0;
       uint32_t ph = 0, pph = 0;
       bool ok = true;
       for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
@@ -936,10 +940,14 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
             tc_commit2(&bar_empty[b]);
           }
           __syncwarp();
+          ++issued;
           if (++b == S) b = 0, ph ^= 1;
           if (++p == 2) p = 0, pph ^= 1;
         }
       }
+      // and so do the other CTA's last arrivals on bar_pfree (relaxed: no barrier at the end orders them)
+      for (int i = max(0, issued - 2); ok && i < issued; ++i)
+        ok = wait_bar_warp(&bar_pfree[i % 2], (i / 2) & 1, abrt);
       if (*abrt) {  // let issued MMAs finish before TMEM is freed
         volatile int never = 0;
         if (elect_one()) tc_commit2(&bar_drain);
