@@ -122,9 +122,13 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
-// wait_bar of a whole warp, which takes the same way afterwards.
+// wait_bar of a whole warp, which takes the same way afterwards. The lanes may
+// wait for different barriers: what one of them acquired is ordered for all by
+// the __syncwarp (a vote orders no memory).
 __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
+  const bool ok = __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
+  __syncwarp();
+  return ok;
 }
 
 __device__ __forceinline__ void put_out(const Fp8Out& o, size_t at, float v) {
