@@ -521,6 +521,20 @@ int hxq_fp8_info(hxq_fp8_t h, int* n_experts, int* N, int* K);
  */
 int hxq_fp8_check(hxq_fp8_t h);
 
+/*
+ * Test hook, not for production use: hxq_fp8_forward (offsets NULL) or
+ * hxq_fp8_forward_grouped with fp32 y and no bias, every pipeline wait bounded
+ * at about wait_limit_us microseconds (1 .. 2e6; counted as 2000 cycles of the
+ * SM's clock each) and the activations of stage `withhold_stage` (>= 0, or -1
+ * for none) of each CTA never requested, so that the wait for them runs
+ * out: the CTAs let what they issued end, free their tensor memory and return,
+ * and the next hxq_fp8_check reports HXQ_ETIMEOUT. y is not written meaningfully
+ * then. Nothing faults or hangs: every wait is bounded. Errors as those calls',
+ * and HXQ_EINVAL for a stage or limit outside these ranges.
+ */
+int hxq_test_fp8_forward_withheld(hxq_fp8_t h, const uint8_t* xq, const float* xs, const int32_t* offsets, float* y,
+                                  int M, int withhold_stage, unsigned wait_limit_us, void* stream);
+
 /* Free a handle (NULL is ignored). Synchronises the device first. */
 void hxq_fp8_destroy(hxq_fp8_t h);
 

@@ -27,3 +27,16 @@ def test_rows_next_to_2_31_are_refused(M, grouped):
     else:
         rc = m.lib.hxq_fp8_forward(h, p, p, None, p, 0, M, None)
     assert rc == m.HXQ_EINVAL
+
+
+@pytest.mark.parametrize("bad", [dict(h=False), dict(stage=-2), dict(limit=0), dict(limit=2000001), dict(M=-1),
+                                 dict(x=False)], ids=str)
+def test_withheld_hook_refuses(bad):
+    import vq_compressed_linear_b200 as m
+    a = {**dict(h=True, stage=1, limit=1000, M=4, x=True), **bad}
+    raw = _handle(1, 16)
+    buf = np.zeros(64, np.float64)
+    p = ctypes.c_void_p((buf.ctypes.data + 15) // 16 * 16)
+    h = ctypes.c_void_p(raw.ctypes.data) if a["h"] else None
+    assert m.lib.hxq_test_fp8_forward_withheld(h, p if a["x"] else None, p, None, p, a["M"], a["stage"], a["limit"],
+                                               None) == m.HXQ_EINVAL

@@ -28,3 +28,36 @@ def test_pairs_with_one_empty_half(hxq, out):
         r = slice(e * n, (e + 1) * n)
         check_product(ys[0][r], dense_x(xq[r], xs[r], K), dense_w(wq[e], ws[e]), None, f"expert {e}")
     check_product(zs[0], dense_x(xq[:1400], xs[:1400], K), dense_w(wq[0], ws[0]), None)
+
+
+# (M, N, K, rows per expert or None): each kernel, one CTA and clusters and pairs, and the experts' forms
+WITHHELD = [(1, 11008, 1024, None), (29, 2048, 4096, None), (60, 2048, 4096, None), (512, 2048, 2048, None),
+            (16, 1024, 2048, [3, 0, 9, 4]), (200, 512, 2048, [50] * 4), (4800, 1024, 512, [120] * 40)]
+
+
+@pytest.mark.parametrize("M,N,K,counts", WITHHELD, ids=lambda v: str(v)[:12])
+@pytest.mark.parametrize("stage", [0, 1])
+def test_withheld_activations_time_out_then_recover(hxq, M, N, K, counts, stage):
+    """Each CTA's stage never gets its activations: the waits run out (1 ms), the CTAs let go of what they hold and
+    return, check reports it once, and the next products on the handle are right."""
+    import torch
+    xq, xs = make_activation(1, M, K)
+    wq, ws = make_weights(2, len(counts or [1]), N, K)
+    lin = hxq.Fp8Linear(wq, ws) if counts else hxq.Fp8Linear(wq[0], ws[0])
+    off = offsets_of(counts) if counts else None
+    run = (lambda: lin.forward_grouped(xq, xs, off)) if counts else (lambda: lin.forward(xq, xs))
+    want = run()
+    check_product(want[:1], dense_x(xq[:1], xs[:1], K), dense_w(wq[0], ws[0]), None)
+    lin.check()
+    y = torch.empty_like(want)
+    hxq.hxq_test_fp8_forward_withheld(lin.handle, xq, xs, off, y, M, -1, 100000)
+    torch.cuda.synchronize()
+    lin.check()
+    assert torch.equal(y, want)  # nothing withheld: the product
+    hxq.hxq_test_fp8_forward_withheld(lin.handle, xq, xs, off, y, M, stage, 1000)
+    torch.cuda.synchronize()
+    assert hxq.lib.hxq_fp8_check(lin.handle) == hxq.HXQ_ETIMEOUT
+    assert hxq.lib.hxq_fp8_check(lin.handle) == hxq.HXQ_OK  # reported once, then cleared
+    for _ in range(3):
+        assert torch.equal(run(), want)
+    lin.check()

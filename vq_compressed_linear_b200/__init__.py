@@ -95,6 +95,8 @@ lib.hxq_fp8_info.argtypes = [_vp, ctypes.POINTER(_i), ctypes.POINTER(_i), ctypes
 lib.hxq_fp8_info.restype = _i
 lib.hxq_fp8_check.argtypes = [_vp]
 lib.hxq_fp8_check.restype = _i
+lib.hxq_test_fp8_forward_withheld.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _i, ctypes.c_uint, _vp]
+lib.hxq_test_fp8_forward_withheld.restype = _i
 lib.hxq_fp8_destroy.argtypes = [_vp]
 lib.hxq_fp8_destroy.restype = None
 lib.hxq_linear_destroy.argtypes = [_vp]
@@ -106,7 +108,8 @@ EXPORTED = ("hxq_linear_create", "hxq_linear_forward", "hxq_linear_forward_ex", 
             "hxq_linear_forward_host", "hxq_linear_forward_noalloc", "hxq_group_create", "hxq_group_forward", "hxq_group_destroy", "hxq_assign", "hxq_kmeans", "hxq_encode", "hxq_decode",
             "hxq_linear_check", "hxq_test_forward_withheld", "hxq_linear_info", "hxq_linear_destroy",
             "hxq_fp8_ld", "hxq_fp8_quantize", "hxq_fp8_swiglu", "hxq_fp8_encode", "hxq_rmsnorm", "hxq_fp8_create",
-            "hxq_fp8_forward", "hxq_fp8_forward_grouped", "hxq_fp8_info", "hxq_fp8_check", "hxq_fp8_destroy",
+            "hxq_fp8_forward", "hxq_fp8_forward_grouped", "hxq_fp8_info", "hxq_fp8_check",
+            "hxq_test_fp8_forward_withheld", "hxq_fp8_destroy",
             "hxq_strerror")
 
 
@@ -296,6 +299,15 @@ def hxq_fp8_info(h) -> tuple[int, int, int]:
 
 def hxq_fp8_check(h) -> None:
     _check(lib.hxq_fp8_check(h), "hxq_fp8_check")
+
+
+def hxq_test_fp8_forward_withheld(h, xq, xs, offsets, y, M, withhold_stage, wait_limit_us, stream=None) -> None:
+    """Test hook: a product with one stage's activations withheld (-1: none) and
+    every pipeline wait bounded at wait_limit_us (the next hxq_fp8_check
+    reports HXQ_ETIMEOUT)"""
+    _check(lib.hxq_test_fp8_forward_withheld(h, _ptr(xq), _ptr(xs), _ptr(offsets), _ptr(y), int(M),
+                                             int(withhold_stage), int(wait_limit_us), _stream(stream)),
+           "hxq_test_fp8_forward_withheld")
 
 
 def hxq_fp8_destroy(h) -> None:

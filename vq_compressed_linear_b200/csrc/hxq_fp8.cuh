@@ -51,9 +51,13 @@ struct Fp8Out {
   int bf16;
 };
 
-// offsets: device int32 [n_experts + 1], or null for one expert with all M rows.
+// offsets: device int32 [n_experts + 1], or null for one expert with all M
+// rows. wait_cycles bounds every pipeline wait (about 2 s by default);
+// withhold >= 0 is a test hook (that stage of each CTA never gets its
+// activations).
+constexpr long long kFp8WaitCycles = 4000000000ll;
 cudaError_t launch_fp8_mm(const hxq_fp8& h, const uint8_t* xq, const float* xs, const int* offsets, const Fp8Out& out,
-                          int M, cudaStream_t s);
+                          int M, cudaStream_t s, long long wait_cycles = kFp8WaitCycles, int withhold = -1);
 cudaError_t launch_fp8_retile(const uint8_t* src, uint8_t* dst, int N, int K, cudaStream_t s);
 cudaError_t launch_fp8_quantize(const void* x, int bf16, int64_t rows, int cols, uint8_t* q, float* scales,
                                 cudaStream_t s);

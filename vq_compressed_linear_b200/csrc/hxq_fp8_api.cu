@@ -61,7 +61,7 @@ void free_fp8(hxq_fp8* h) {
 }
 
 int mm_impl(hxq_fp8_t h, const uint8_t* xq, const float* xs, const int32_t* offsets, const float* bias, void* y,
-            int out_type, int M, void* stream) {
+            int out_type, int M, void* stream, long long wait_cycles = hxq::kFp8WaitCycles, int withhold = -1) {
   if (!is_type(out_type) || M < 0) return HXQ_EINVAL;
   if (M == 0) return check_current(h->device);
   if (!xq || !xs || !y) return HXQ_EINVAL;
@@ -72,7 +72,8 @@ int mm_impl(hxq_fp8_t h, const uint8_t* xq, const float* xs, const int32_t* offs
   if (M > INT_MAX - 255 || ((int64_t)M + h->n_experts) * h->n_tiles >= kMaxBlocks) return HXQ_EINVAL;
   if (const int rc = check_current(h->device)) return rc;
   const hxq::Fp8Out out{y, bias, out_type == HXQ_TYPE_BF16 ? 1 : 0};
-  return fp8_status(hxq::launch_fp8_mm(*h, xq, xs, offsets, out, M, static_cast<cudaStream_t>(stream)));
+  return fp8_status(hxq::launch_fp8_mm(*h, xq, xs, offsets, out, M, static_cast<cudaStream_t>(stream), wait_cycles,
+                                       withhold));
 }
 
 }  // namespace
@@ -218,6 +219,13 @@ int hxq_fp8_check(hxq_fp8_t h) {
   cudaMemset(h->d_status, 0, sizeof(int));
   cudaDeviceSynchronize();
   return HXQ_ETIMEOUT;
+}
+
+int hxq_test_fp8_forward_withheld(hxq_fp8_t h, const uint8_t* xq, const float* xs, const int32_t* offsets, float* y,
+                                  int M, int withhold_stage, unsigned wait_limit_us, void* stream) {
+  if (!h || (!offsets && h->n_experts != 1)) return HXQ_EINVAL;
+  if (withhold_stage < -1 || wait_limit_us < 1 || wait_limit_us > 2000000u) return HXQ_EINVAL;
+  return mm_impl(h, xq, xs, offsets, nullptr, y, HXQ_TYPE_F32, M, stream, wait_limit_us * 2000ll, withhold_stage);
 }
 
 void hxq_fp8_destroy(hxq_fp8_t h) {

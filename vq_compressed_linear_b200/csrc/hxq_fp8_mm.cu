@@ -39,6 +39,8 @@ struct MmArgs {
   Fp8Out out;
   int M, N, K, n_tiles, n_blocks, n_experts;
   int* status;
+  long long wait_cycles;  // limit of every wait, in cycles of the SM's clock
+  int withhold;           // test hook: that stage of each CTA never gets its activations (-1: none)
 };
 
 // ---- PTX that only these kernels use ----------------------------------------
@@ -83,9 +85,12 @@ __device__ __forceinline__ void mbar_arrive_rank(uint64_t* bar, uint32_t rank) {
 __device__ __forceinline__ void mbar_signal_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// Waits, bounded at kWaitCycles of the SM's clock (about 2 s): false, with
-// *abort set, when the limit passes or another thread of the CTA gave up.
-constexpr long long kWaitCycles = 4000000000ll;
+// Waits, bounded: false, with *abort set, when the limit passes or another
+// thread of the CTA gave up.
+struct Patience {
+  volatile int* abort;
+  long long limit;  // cycles of the SM's clock
+};
 
 template <bool CLUSTER>
 __device__ __forceinline__ bool try_bar(uint64_t* bar, uint32_t parity) {
@@ -101,15 +106,15 @@ __device__ __forceinline__ bool try_bar(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Patience w) {
   if (try_bar<CLUSTER>(bar, parity)) return true;
   const long long t0 = clock64();
   for (uint32_t i = 1;; ++i) {
     if (try_bar<CLUSTER>(bar, parity)) return true;
     if ((i & 31) == 0) {
-      if (*abort) return false;
-      if (clock64() - t0 > kWaitCycles) {
-        *abort = 1;
+      if (*w.abort) return false;
+      if (clock64() - t0 > w.limit) {
+        *w.abort = 1;
         return false;
       }
     }
@@ -125,10 +130,22 @@ __device__ __forceinline__ bool elect_one() {
 // wait_bar of a whole warp, which takes the same way afterwards. The lanes may
 // wait for different barriers: what one of them acquired is ordered for all by
 // the __syncwarp (a vote orders no memory).
-__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  const bool ok = __all_sync(0xffffffffu, wait_bar(bar, parity, abort));
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, Patience w) {
+  const bool ok = __all_sync(0xffffffffu, wait_bar(bar, parity, w));
   __syncwarp();
   return ok;
+}
+// After an abort: a wait of its own for what this CTA still has in flight.
+__device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity, long long limit) {
+  volatile int mine = 0;
+  wait_bar(bar, parity, Patience{&mine, limit});
+}
+// After an abort, when every CTA of the cluster has stopped: what is in flight
+// between them (arrivals, sums, copies counted in another CTA) has no barrier
+// that this CTA could wait for. A millisecond is a thousand times what it takes.
+__device__ __forceinline__ void settle() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < 2000000ll) __nanosleep(10000);
 }
 
 __device__ __forceinline__ void put_out(const Fp8Out& o, size_t at, float v) {
@@ -261,13 +278,13 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
   __shared__ uint64_t bar_recv[4], bar_rfree[4];  // per quadrant of rows
   __shared__ __align__(16) float sc[SC][KP][BN + 4];  // a block's activation scales, then the tile's scale
   __shared__ uint32_t tmem_sh;
-  __shared__ int abort_sh;
+  __shared__ int abort_sh, issued_sh;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = cluster > 1 ? (int)cluster_rank() : 0;
   const int my = blockIdx.x / cluster, n_clusters = gridDim.x / cluster;
   const int kb0 = rank * a.n_blocks / cluster, kb1 = (rank + 1) * a.n_blocks / cluster;
-  volatile int* abrt = &abort_sh;
+  const Patience pat{&abort_sh, a.wait_cycles};
 
   pdl_launch_dependents();
   // a stage's weights and activations into its slot
@@ -341,25 +358,23 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
       if (first) {
         first = false;
         if (elect_one())
-          for (int i = 0; i < ahead; ++i) load_x(w.row, kb0 + i * KP, i);
+          for (int i = 0; i < ahead; ++i)
+            if (i != a.withhold) load_x(w.row, kb0 + i * KP, i);
         __syncwarp();
         kb += ahead * KP;
       }
       for (; kb < kb1; kb += KP) {
-        if (!(ok = wait_bar_warp(&bar_p[b], ph ^ 1, abrt))) break;
+        if (!(ok = wait_bar_warp(&bar_p[b], ph ^ 1, pat))) break;
         if (elect_one()) {
           load_w(t0, kb, b);
-          load_x(w.row, kb, b);
+          if (issued != a.withhold) load_x(w.row, kb, b);
         }
         __syncwarp();
         ++issued;
         if (++b == S) b = 0, ph ^= 1;
       }
     }
-    if (*abrt) {  // let the copies this warp issued land before the CTA ends
-      volatile int never = 0;
-      for (int i = max(0, issued - S); i < issued; ++i) wait_bar(&bar_full[i % S], (i / S) & 1, &never);
-    }
+    if (lane == 0) issued_sh = issued;
   } else if (warp == 1) {
     int b = 0;
     uint32_t ph = 0;
@@ -368,7 +383,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
       const uint32_t idesc = idesc_e4m3(128, (w.ntok + 15) / 16 * 16);
       for (int kb = kb0; kb < kb1; kb += KP) {
         // (odd lanes wait for the operands, even lanes for the TMEM slot)
-        if (!(ok = wait_bar_warp(lane & 1 ? &bar_full[b] : &bar_pfree[b], lane & 1 ? ph : ph ^ 1, abrt))) break;
+        if (!(ok = wait_bar_warp(lane & 1 ? &bar_full[b] : &bar_pfree[b], lane & 1 ? ph : ph ^ 1, pat))) break;
         tc_fence_after();
         if (elect_one()) {
           const uint64_t wd = smem_desc(smem_u32(ring + b * C::kStage));
@@ -388,12 +403,6 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
         if (++b == S) b = 0, ph ^= 1;
       }
     }
-    if (*abrt) {  // let issued MMAs finish before TMEM is freed
-      volatile int never = 0;
-      if (elect_one()) tc_commit(&bar_drain);
-      __syncwarp();
-      wait_bar(&bar_drain, 0, &never);
-    }
   } else if (warp == 3) {
     int p = 0;
     uint32_t ph = 0;
@@ -403,7 +412,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
       const float* ws = a.ws + (size_t)(w.e * a.n_tiles + w.tile) * a.n_blocks;
       const float* xs = a.xs + (size_t)w.row * a.n_blocks;
       for (int kb = kb0; kb < kb1; kb += KP) {
-        if (!(ok = wait_bar_warp(&bar_sfree[p], ph ^ 1, abrt))) break;
+        if (!(ok = wait_bar_warp(&bar_sfree[p], ph ^ 1, pat))) break;
 #pragma unroll
         for (int i = lane; i < BN * KP; i += 32) {  // (columns past the tokens are never used)
           const int c = i / KP, j = i % KP;
@@ -434,7 +443,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
       auto live = [&](int i) { return 16 * (i * G + grp) < w.ntok; };
       for (int kb = kb0; kb < kb1; kb += KP) {
         const int nk = min(KP, kb1 - kb);
-        if (!(ok = wait_bar_warp(lane & 1 ? &bar_p[p] : &bar_s[sp], lane & 1 ? pph : sph, abrt))) break;
+        if (!(ok = wait_bar_warp(lane & 1 ? &bar_p[p] : &bar_s[sp], lane & 1 ? pph : sph, pat))) break;
         tc_fence_after();
         // the next block's P loads while this one's is added
         uint32_t d[2][NC][16];
@@ -491,7 +500,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
         continue;
       }
       // this rank's sums of column c to slot [rank][c % own] of the rank c / own that adds column c
-      if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(&bar_rfree[q], uph ^ 1, abrt)))) break;
+      if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(&bar_rfree[q], uph ^ 1, pat)))) break;
       const uint32_t mine = smem_u32(recv) + (uint32_t)(rank * own * kFp8Block + r) * 4u;
 #pragma unroll
       for (int i = 0; i < NC; ++i)
@@ -505,7 +514,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
         }
       __syncwarp();
       if (lane < cluster) mbar_arrive_rank(&bar_recv[q], lane);
-      if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(&bar_recv[q], uph, abrt)))) break;
+      if (!(ok = __all_sync(0xffffffffu, wait_bar<true>(&bar_recv[q], uph, pat)))) break;
       const int mine_n = min(own, w.ntok - rank * own);
 #pragma unroll 2
       for (int c = grp; c < mine_n; c += G) {
@@ -524,15 +533,31 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
 
   tc_fence_before();
   __syncthreads();
+  // Every warp has stopped, and what they issued is known: after an abort the
+  // copies land and the MMAs finish before shared memory and TMEM are let go.
+  const bool aborted = *pat.abort != 0;
+  if (aborted) {
+    if (warp == 0) {
+      const int n = issued_sh;
+      for (int i = max(0, n - S); i < n; ++i) drain_bar(&bar_full[i % S], (i / S) & 1, a.wait_cycles);
+    } else if (warp == 1) {
+      if (elect_one()) tc_commit(&bar_drain);
+      __syncwarp();
+      drain_bar(&bar_drain, 0, a.wait_cycles);
+    }
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusWaitTimeout);
+    tc_fence_before();
+    __syncthreads();
+  }
   if (cluster > 1) cluster_arrive_relaxed();
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
-  if (*abrt && threadIdx.x == 0) atomicOr(a.status, kStatusWaitTimeout);
   if (cluster > 1) {  // no CTA leaves while another may still reach into its shared memory
     __syncwarp();
     cluster_wait();
+    if (aborted) settle();
   }
 }
 
@@ -752,6 +777,11 @@ __device__ __forceinline__ void tc_commit2(uint64_t* bar) {
       ::"r"(smem_u32(bar)), "h"((uint16_t)3)
       : "memory");
 }
+// The same on this CTA's barrier alone.
+__device__ __forceinline__ void tc_commit2_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               ::"r"(smem_u32(bar)) : "memory");
+}
 // This CTA's shared memory <- global; the bytes are counted on the barrier `bar` (an address from map_to_rank) of
 // either CTA of the pair.
 __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* tmap, uint32_t bar, int c0, int c1) {
@@ -852,12 +882,12 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
   __shared__ uint64_t bar_s[kWideSc], bar_sfree[kWideSc];
   __shared__ float sc[kWideSc][128 + 2];  // a block's activation scales, then the two tiles' scales
   __shared__ uint32_t tmem_sh;
-  __shared__ int abort_sh;
+  __shared__ int abort_sh, issued_sh;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-  volatile int* abrt = &abort_sh;
+  const Patience pat{&abort_sh, a.wait_cycles};
 
   pdl_launch_dependents();
   if (warp == 0 && elect_one()) {
@@ -906,12 +936,12 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
         const int w0 = (w.e * a.n_tiles + w.tile(off)) * a.n_blocks * kFp8Block + w.tile_row(off);
         const int x0 = w.row + rank * 128;
         for (int kb = 0; kb < a.n_blocks; ++kb) {
-          if (!(ok = wait_bar_warp(&bar_empty[b], ph ^ 1, abrt))) break;
+          if (!(ok = wait_bar_warp(&bar_empty[b], ph ^ 1, pat))) break;
           if (elect_one()) {
             if (rank == 0) mbar_arrive_expect_tx(&bar_full[b], 2 * (kFp8TileBytes + rows * kFp8Block));
             const uint32_t bar = map_to_rank(smem_u32(&bar_full[b]), 0);
             uint8_t* slot = ring + b * kWideStage;
-            tma_load_2d_pair(slot, &maps.x, bar, kb * kFp8Block, x0);
+            if (issued != a.withhold) tma_load_2d_pair(slot, &maps.x, bar, kb * kFp8Block, x0);
             tma_load_2d_pair(slot + kFp8TileBytes, tw, bar, 0, w0 + kb * kFp8Block);
           }
           __syncwarp();
@@ -922,11 +952,8 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
       // The leading CTA's tensor core arrives on this CTA's bar_empty after bar_p, which the adders wait for: the last
       // stages' arrivals land before the CTA leaves its shared memory.
       for (int i = max(0, issued - S); ok && i < issued; ++i)
-        ok = wait_bar_warp(&bar_empty[i % S], (i / S) & 1, abrt);
-      if (*abrt && rank == 0) {  // let the copies land before the CTA ends (the other CTA's are counted here too)
-        volatile int never = 0;
-        for (int i = max(0, issued - S); i < issued; ++i) wait_bar(&bar_full[i % S], (i / S) & 1, &never);
-      }
+        ok = wait_bar_warp(&bar_empty[i % S], (i / S) & 1, pat);
+      if (lane == 0) issued_sh = issued;
     } else if (warp == 1 && rank == 0) {
       int b = 0, p = 0, issued = 0;
       uint32_t ph = 0, pph = 0;
@@ -935,7 +962,7 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
         const uint32_t idesc = idesc_e4m3(256, w.width);
         for (int kb = 0; kb < a.n_blocks; ++kb) {
           const uint64_t xd = smem_desc(smem_u32(ring + b * kWideStage)), wd = xd + (kFp8TileBytes >> 4);
-          if (!(ok = wait_bar_warp(lane & 1 ? &bar_full[b] : &bar_pfree[p], lane & 1 ? ph : pph ^ 1, abrt))) break;
+          if (!(ok = wait_bar_warp(lane & 1 ? &bar_full[b] : &bar_pfree[p], lane & 1 ? ph : pph ^ 1, pat))) break;
           tc_fence_after();
           if (elect_one()) {
 #pragma unroll
@@ -951,13 +978,7 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
       }
       // and so do the other CTA's last arrivals on bar_pfree (relaxed: no barrier at the end orders them)
       for (int i = max(0, issued - 2); ok && i < issued; ++i)
-        ok = wait_bar_warp(&bar_pfree[i % 2], (i / 2) & 1, abrt);
-      if (*abrt) {  // let issued MMAs finish before TMEM is freed
-        volatile int never = 0;
-        if (elect_one()) tc_commit2(&bar_drain);
-        __syncwarp();
-        wait_bar(&bar_drain, 0, &never);
-      }
+        ok = wait_bar_warp(&bar_pfree[i % 2], (i / 2) & 1, pat);
     } else if (warp == 3) {
       int sp = 0;
       uint32_t sph = 0;
@@ -966,7 +987,7 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
       for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
         const float* ws = a.ws + (size_t)(w.e * a.n_tiles + w.tile(lane * w.width / 2)) * a.n_blocks;
         for (int kb = 0; kb < a.n_blocks; ++kb) {
-          if (!(ok = wait_bar_warp(&bar_sfree[sp], sph ^ 1, abrt))) break;
+          if (!(ok = wait_bar_warp(&bar_sfree[sp], sph ^ 1, pat))) break;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int t = i * 32 + lane, tok = rank * 128 + t;  // (rows past the tokens are never stored)
@@ -994,7 +1015,7 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.f, 0.f);
       for (int kb = 0; kb < a.n_blocks; ++kb) {
-        if (!(ok = wait_bar_warp(lane & 1 ? &bar_p[p] : &bar_s[sp], lane & 1 ? pph : sph, abrt))) break;
+        if (!(ok = wait_bar_warp(lane & 1 ? &bar_p[p] : &bar_s[sp], lane & 1 ? pph : sph, pat))) break;
         tc_fence_after();
         const uint32_t at = lane_base + p * 256 + col0;
         const float s = sc[sp][q * 32 + lane] * sc[sp][128 + half];
@@ -1066,11 +1087,27 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
 
   tc_fence_before();
   __syncthreads();
-  if (*abrt && threadIdx.x == 0) atomicOr(a.status, kStatusWaitTimeout);
+  // as in fp8_skinny_kernel; the other CTA's copies are counted here, too
+  const bool aborted = *pat.abort != 0;
+  if (aborted) {
+    if (warp == 0 && rank == 0) {
+      const int n = issued_sh;
+      for (int i = max(0, n - S); i < n; ++i) drain_bar(&bar_full[i % S], (i / S) & 1, a.wait_cycles);
+    } else if (warp == 1 && rank == 0) {
+      if (elect_one()) tc_commit2_own(&bar_drain);
+      __syncwarp();
+      drain_bar(&bar_drain, 0, a.wait_cycles);
+    }
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusWaitTimeout);
+    tc_fence_before();
+    __syncthreads();
+  }
   // neither CTA frees TMEM or leaves while the other may still use its memory
   __syncwarp();
   cluster_arrive_relaxed();
   cluster_wait();
+  if (aborted) settle();
+  __syncwarp();
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc2(tmem, 512);
@@ -1174,8 +1211,9 @@ cudaError_t fp8_tensor_map(CUtensorMap* tm, const void* base, uint64_t cols, uin
 }
 
 cudaError_t launch_fp8_mm(const hxq_fp8& h, const uint8_t* xq, const float* xs, const int* offsets, const Fp8Out& out,
-                          int M, cudaStream_t s) {
-  const MmArgs a{xs, h.d_ws, offsets, out, M, h.N, h.K, h.n_tiles, h.n_blocks, h.n_experts, h.d_status};
+                          int M, cudaStream_t s, long long wait_cycles, int withhold) {
+  const MmArgs a{xs,     h.d_ws,     offsets,    out,         M,          h.N,        h.K,
+                 h.n_tiles, h.n_blocks, h.n_experts, h.d_status, wait_cycles, withhold};
   return offsets ? launch_mm<true>(h, xq, a, s) : launch_mm<false>(h, xq, a, s);
 }
 
