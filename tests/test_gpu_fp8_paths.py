@@ -61,3 +61,31 @@ def test_withheld_activations_time_out_then_recover(hxq, M, N, K, counts, stage)
     for _ in range(3):
         assert torch.equal(run(), want)
     lin.check()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1024, 512), (20, 256, 2048), (512, 2048, 2048)])
+def test_waits_do_not_count_the_previous_kernel(hxq, M, N, K):
+    """A product launched early behind a kernel that releases its dependents at once and then runs for longer than the
+    product's waits may take: it waits for that kernel's end first, and then runs."""
+    import torch
+    xq, xs = make_activation(1, M, K)
+    wq, ws = make_weights(2, 1, N, K)
+    lin = hxq.Fp8Linear(wq[0], ws[0])
+    want = lin.forward(xq, xs)
+    # two rows of 2^25 columns: two CTAs, some milliseconds, and nearly every SM free for the product
+    x = torch.ones(2, 2**25, device="cuda")
+    y = torch.empty(2, 2**25, dtype=torch.bfloat16, device="cuda")
+    hxq.rmsnorm(x, y=y)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    hxq.rmsnorm(x, y=y)
+    b.record()
+    torch.cuda.synchronize()
+    limit = int(a.elapsed_time(b) * 1000 / 4)
+    assert limit > 200, "the kernel in front is too short for this test"
+    got = torch.empty_like(want)
+    hxq.rmsnorm(x, y=y)
+    hxq.hxq_test_fp8_forward_withheld(lin.handle, xq, xs, None, got, M, -1, limit)
+    torch.cuda.synchronize()
+    lin.check()
+    assert torch.equal(got, want)

@@ -379,6 +379,7 @@ fp8_skinny_kernel(const __grid_constant__ CUtensorMap tmw, const __grid_constant
     int b = 0;
     uint32_t ph = 0;
     bool ok = true;
+    pdl_wait();  // x is loaded after it: the previous kernel's time does not count against the first wait
     for (Walk<BN, GROUPED> w(R, a, my, n_clusters); ok && w.get(R, a); w.next()) {
       const uint32_t idesc = idesc_e4m3(128, (w.ntok + 15) / 16 * 16);
       for (int kb = kb0; kb < kb1; kb += KP) {
@@ -958,6 +959,7 @@ fp8_wide_kernel(const __grid_constant__ WideMaps maps, MmArgs a, int tma_out) {
       int b = 0, p = 0, issued = 0;
       uint32_t ph = 0, pph = 0;
       bool ok = true;
+      pdl_wait();  // x is loaded after it: the previous kernel's time does not count against the first wait
       for (WideWalk w(R, a, GROUPED, pair, pairs); ok && w.get(R, a, GROUPED); w.item += w.step) {
         const uint32_t idesc = idesc_e4m3(256, w.width);
         for (int kb = 0; kb < a.n_blocks; ++kb) {
