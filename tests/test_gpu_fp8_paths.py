@@ -2,7 +2,8 @@
 again, pieces and pairs that end early. Forms and tolerances are those of test_gpu_fp8."""
 import pytest
 
-from test_gpu_fp8 import (check_product, dense_w, dense_x, make_activation, make_weights, offsets_of)
+from test_gpu_fp8 import (DELTA, check_bytes, check_product, check_y, codes, dense_w, dense_x, dtype, make_activation,
+                          make_weights, offsets_of, randn, ref_norm, unaligned)
 
 pytestmark = pytest.mark.gpu
 
@@ -89,3 +90,22 @@ def test_waits_do_not_count_the_previous_kernel(hxq, M, N, K):
     torch.cuda.synchronize()
     lin.check()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [8, 250, 3000, 10008, 33000])
+def test_rmsnorm_padding_is_zero_whatever_the_root(hxq, xt, K):
+    """Bytes past K are 0 in rows whose root is NaN, infinite (zeros without eps) or 0, too."""
+    x = randn(K, 5, K)
+    x[1, 3] = float("nan")
+    x[2, 4] = float("inf")
+    x[3] = 0
+    x = x.to(dtype(xt))
+    for t in (x, unaligned(x)):
+        for eps in (0.0, 1e-6):
+            q, s, y, _ = hxq.rmsnorm(t, None, eps, want="qy")
+            assert codes(q).shape[1] > K and not codes(q)[:, K:].any()
+            _, h = ref_norm(x, None, None, eps)
+            check_bytes(q[[0, 4]], s[[0, 4]], h[[0, 4]], K, DELTA)
+            assert ((codes(q)[1, :K] & 0x7F) == 0x7F).all()
+            check_y(y[[0, 3, 4]], h[[0, 3, 4]])

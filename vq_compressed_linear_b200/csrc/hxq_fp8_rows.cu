@@ -394,6 +394,8 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t
       }
     }
     if (isinf(amax)) no_infinities(h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = j < n ? h[j] : 0.f;  // (the row's padding, where the root is not finite)
     put8(a.q + row * ld, ld, c, h, inv);
     const int b = c / kFp8Block;
     if ((threadIdx.x & (kLanesPerBlock - 1)) == 0 && b < kb) a.scales[row * kb + b] = s;
@@ -780,6 +782,10 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
             if (pass == 0) continue;
             if (a.y && far) store8<true, true>(a.y, row * cols + c, cols - c, v);
             if (isinf((float)m)) no_infinities(v);
+            if (c >= cols) {  // the row's padding, where the root is not finite
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = 0.f;
+            }
             if (a.q) put8(a.q + row * ld, ld, c, v, inv);
           }
           if (pass == 0) {
@@ -806,7 +812,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
       const float s = fp8_scale(amax, &inv);
       uint8_t* q = a.q + row * ld;
 #pragma unroll
-      for (int k = 0; k < P; ++k) put8(q, ld, c0 + kStep * k, t[k], rstd * inv);
+      for (int k = 0; k < P; ++k) put8(q, ld, c0 + kStep * k, t[k], c0 + kStep * k < cols ? rstd * inv : 0.f);
       if (tid % L == 0 && blk < kb) a.scales[row * kb + blk] = s;
     }
     d = d + 1 == D ? 0 : d + 1;
