@@ -109,3 +109,36 @@ def test_rmsnorm_padding_is_zero_whatever_the_root(hxq, xt, K):
             check_bytes(q[[0, 4]], s[[0, 4]], h[[0, 4]], K, DELTA)
             assert ((codes(q)[1, :K] & 0x7F) == 0x7F).all()
             check_y(y[[0, 3, 4]], h[[0, 3, 4]])
+
+
+@pytest.mark.parametrize("xt,rt", [("f32", None), ("bf16", None), ("f32", "bf16"), ("bf16", "bf16")])
+@pytest.mark.parametrize("K", [256, 250, 3000, 10000, 33000])
+def test_rmsnorm_rows_of_subnormals_without_eps(hxq, xt, rt, K):
+    """1 / root beyond fp32's end: y and the 8 bits are ordinary all the same, zeros stay zeros, and a large weight
+    or one of 0 changes nothing of that. Rows of zeros are 0 / 0."""
+    import torch
+    x = randn(K, 7, K)
+    x[0] *= 1e-40
+    x[1] *= 1e-42
+    x[2, 1:] = 0
+    x[2, 0] = 2.0 ** -130
+    x[3] *= 1e-40
+    x[3, :128] = 0
+    x[4] *= 1e-38  # (just inside)
+    x[5] = 0
+    x = x.to(dtype(xt))
+    res = None
+    if rt:  # t = x + residual is x, with its signs as they are
+        res = torch.zeros(7, K, device="cuda", dtype=dtype(rt))
+    for big in (1.0, 2.0 ** 60):
+        w = (1 + randn(K + 1, K, scale=0.2)) * big
+        w[7], w[200] = 0, 0
+        t, h = ref_norm(x, res, w, 0.0)
+        for copy in (lambda v: v, unaligned):
+            q, s, y, total = hxq.rmsnorm(copy(x), w, 0.0, residual=res, want="qy")
+            _, _, y1, _ = hxq.rmsnorm(copy(x), w, 0.0, residual=res, want="y")
+            if res is not None:
+                assert torch.equal(total, t)
+            check_bytes(q, s, h, K, DELTA)
+            check_y(y, h)
+            assert torch.equal(y1.view(torch.int16), y.view(torch.int16))

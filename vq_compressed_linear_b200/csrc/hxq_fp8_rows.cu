@@ -355,9 +355,15 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// What both norm kernels do with a thread's 8 values t of one chunk (columns
-// c ..), their weights and the row's statistics: h = t rstd g as bf16 and / or
-// 8 bits. mean64(): the mean of squares (plus eps) in 64 bits, asked for by a
+// With eps 0 and a root mean square below 2.9e-39 (a row of subnormal numbers)
+// 1 / root leaves fp32: root() is infinite. Such a row's t are taken times kLift
+// (exact) and its factor divided by it. A row of zeros keeps 0 / 0.
+constexpr double kLift = 0x1p64;
+__device__ __forceinline__ float lifted_root(double mean) { return (float)(1.0 / (sqrt(mean) * kLift)); }
+
+// What the norm kernels do with a thread's 8 values t of one chunk (columns
+// c .., lifted if the row is), their weights and the row's statistics: h = t
+// rstd g as bf16 and / or 8 bits. mean64(): the mean of squares (plus eps) in 64 bits, asked for by a
 // whole warp and only where it decides a scale.
 template <bool VEC, typename Mean64>
 __device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t ld, int kb, int c,
@@ -380,7 +386,8 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t
         unsure = unsure && any != 0.f;
       }
       if (__any_sync(0xffffffffu, unsure)) {
-        const double r = 1.0 / sqrt(mean64());
+        double r = 1.0 / sqrt(mean64());
+        if (isinf((float)r)) r /= kLift;
         double m = 0.0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -536,7 +543,17 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs
     };
     const double mean = fma(sd, inv_cols, (double)a.eps);
     float rstd = root(mean);
-    if (!(mean < 1e37 && mean > 1e-30)) rstd = root(mean64());  // squares beyond the range of fp32
+    if (!(mean < 1e37 && mean > 1e-30)) {  // squares beyond the range of fp32
+      const double m = mean64();
+      rstd = root(m);
+      if (isinf(rstd)) {
+        rstd = lifted_root(m);
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t[i][j] *= (float)kLift;
+      }
+    }
 #pragma unroll
     for (int i = 0; i < NCH; ++i) norm_out<true>(a, row, ld, kb, col(i), t[i], g[i], rstd, mean64);
     if (D == 1) {
@@ -581,11 +598,17 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
   ss = 0.0;
   for (int w = 0; w < T / 32; ++w) ss += part[w];
   const double mean = ss / cols + (double)a.eps;
-  const float rstd = root(mean);
+  float rstd = root(mean);
+  const bool lift = isinf(rstd);
+  if (lift) rstd = lifted_root(mean);
   for (int i = 0; i < iters; ++i) {
     const int c = (i * T + tid) * kVec;
     load_t(i, t);
     if (a.sum) store8<RBF16, VEC>(a.sum, row * cols + c, cols - c, t);
+    if (lift) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] *= (float)kLift;
+    }
     float g[8];
     if (a.weight) {
       load8<false, VEC>(a.weight, c, cols - c, g);
@@ -724,7 +747,17 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
     };
     const double mean = fma(sd, inv_cols, (double)a.eps);
     float rstd = root(mean);
-    if (!(mean < 1e37 && mean > 1e-30)) rstd = root(mean64());  // squares beyond the range of fp32
+    if (!(mean < 1e37 && mean > 1e-30)) {  // squares beyond the range of fp32
+      const double m = mean64();
+      rstd = root(m);
+      if (isinf(rstd)) {
+        rstd = lifted_root(m);
+#pragma unroll
+        for (int k = 0; k < P; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t[k][j] *= (float)kLift;
+      }
+    }
 
     // p = t g, its maximum over the block gives the scale; h = p rstd
     float pm = 0.f;
