@@ -142,3 +142,19 @@ def test_rmsnorm_rows_of_subnormals_without_eps(hxq, xt, rt, K):
             check_bytes(q, s, h, K, DELTA)
             check_y(y, h)
             assert torch.equal(y1.view(torch.int16), y.view(torch.int16))
+
+
+@pytest.mark.parametrize("out", ["y", "q", "scales", "sum"])
+def test_rmsnorm_refuses_each_output_in_pageable_memory(hxq, out):
+    """Outputs that the GPU cannot reach are refused on the host, whichever they are."""
+    import numpy as np
+    import torch
+    x, res = randn(1, 2, 32), randn(2, 2, 32)
+    host = np.zeros(1024, np.uint8)
+    p = {"y": torch.empty(2, 32, dtype=torch.bfloat16, device="cuda"), "q": torch.empty(2, 32, dtype=torch.uint8, device="cuda"),
+         "scales": torch.empty(2, 1, device="cuda"), "sum": torch.empty(2, 32, device="cuda")}
+    at = {k: v.data_ptr() for k, v in p.items()}
+    at[out] = (host.ctypes.data + 15) // 16 * 16
+    rc = hxq.lib.hxq_rmsnorm(x.data_ptr(), 0, res.data_ptr(), at["sum"], 0, None, 1e-6, 2, 32, at["y"], at["q"],
+                             at["scales"], None)
+    assert rc == hxq.HXQ_EINVAL

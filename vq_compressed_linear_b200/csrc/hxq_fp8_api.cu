@@ -3,6 +3,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <new>
 
 #include "hxq_fp8.cuh"
@@ -19,22 +20,25 @@ int fp8_status(cudaError_t e) {
 bool is_type(int t) { return t == HXQ_TYPE_F32 || t == HXQ_TYPE_BF16; }
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// The current device must be the one whose memory `p` is (pinned host memory
-// and managed memory are reachable from any): a kernel launched elsewhere
-// would fault.
-int check_pointer(const void* p) {
+// The current device must be the one whose memory each pointer is (pinned host
+// memory and managed memory are reachable from any): a kernel launched
+// elsewhere would fault. NULL is passed over.
+int check_pointers(std::initializer_list<const void*> all) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
     return HXQ_ECUDA;
   }
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();
-    return HXQ_EINVAL;
+  for (const void* p : all) {
+    if (!p) continue;
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+      cudaGetLastError();
+      return HXQ_EINVAL;
+    }
+    if (a.type == cudaMemoryTypeUnregistered || (a.type == cudaMemoryTypeDevice && a.device != dev)) return HXQ_EINVAL;
   }
-  if (a.type == cudaMemoryTypeUnregistered) return HXQ_EINVAL;
-  return a.type == cudaMemoryTypeDevice && a.device != dev ? HXQ_EINVAL : HXQ_OK;
+  return HXQ_OK;
 }
 
 int check_current(int device) {
@@ -87,7 +91,7 @@ int hxq_fp8_quantize(const void* x, int x_type, int64_t rows, int cols, uint8_t*
   if (rows == 0) return HXQ_OK;
   if (!x || !q || !scales) return HXQ_EINVAL;
   if (!aligned(q, 16) || !aligned(scales, 4) || !aligned(x, x_type == HXQ_TYPE_BF16 ? 2 : 4)) return HXQ_EINVAL;
-  if (const int rc = check_pointer(q)) return rc;
+  if (const int rc = check_pointers({q})) return rc;
   return fp8_status(hxq::launch_fp8_quantize(x, x_type == HXQ_TYPE_BF16, rows, cols, q, scales,
                                              static_cast<cudaStream_t>(stream)));
 }
@@ -97,7 +101,7 @@ int hxq_fp8_swiglu(const void* gate_up, int type, int64_t rows, int cols, uint8_
   if (rows == 0) return HXQ_OK;
   if (!gate_up || !q || !scales) return HXQ_EINVAL;
   if (!aligned(q, 16) || !aligned(scales, 4) || !aligned(gate_up, type == HXQ_TYPE_BF16 ? 2 : 4)) return HXQ_EINVAL;
-  if (const int rc = check_pointer(q)) return rc;
+  if (const int rc = check_pointers({q})) return rc;
   return fp8_status(hxq::launch_fp8_swiglu(gate_up, type == HXQ_TYPE_BF16, rows, cols, q, scales,
                                            static_cast<cudaStream_t>(stream)));
 }
@@ -106,7 +110,7 @@ int hxq_fp8_encode(const void* W, int type, int n_experts, int N, int K, uint8_t
   if (!W || !q || !scales || !is_type(type) || n_experts < 1 || N < 1 || K < 1) return HXQ_EINVAL;
   if ((int64_t)hxq::fp8_blocks(N) * hxq::fp8_blocks(K) >= kMaxBlocks / n_experts) return HXQ_EINVAL;
   if (!aligned(scales, 4) || !aligned(W, type == HXQ_TYPE_BF16 ? 2 : 4)) return HXQ_EINVAL;
-  if (const int rc = check_pointer(q)) return rc;
+  if (const int rc = check_pointers({q})) return rc;
   return fp8_status(hxq::launch_fp8_encode(W, type == HXQ_TYPE_BF16, n_experts, N, K, q, scales,
                                            static_cast<cudaStream_t>(stream)));
 }
@@ -121,7 +125,7 @@ int hxq_rmsnorm(const void* x, int x_type, const void* residual, void* sum, int 
   if (!aligned(x, x_type == HXQ_TYPE_BF16 ? 2 : 4) || !aligned(residual, rt) || !aligned(sum, rt) ||
       !aligned(weight, 4) || !aligned(y_bf16, 2) || !aligned(q, 16) || !aligned(scales, 4))
     return HXQ_EINVAL;
-  if (const int rc = check_pointer(q ? static_cast<const void*>(q) : y_bf16)) return rc;
+  if (const int rc = check_pointers({y_bf16, q, scales, sum})) return rc;
   const hxq::NormArgs a{x, residual, sum, weight, eps, cols, static_cast<uint16_t*>(y_bf16), q, scales};
   return fp8_status(hxq::launch_rmsnorm(a, x_type == HXQ_TYPE_BF16, residual_type == HXQ_TYPE_BF16, rows,
                                         static_cast<cudaStream_t>(stream)));
