@@ -158,3 +158,191 @@ def test_rmsnorm_refuses_each_output_in_pageable_memory(hxq, out):
     rc = hxq.lib.hxq_rmsnorm(x.data_ptr(), 0, res.data_ptr(), at["sum"], 0, None, 1e-6, 2, 32, at["y"], at["q"],
                              at["scales"], None)
     assert rc == hxq.HXQ_EINVAL
+
+
+# ---- persistent loops, rings, clusters with more than one unit --------------------------
+
+NORM_LOOPS = [
+    # (rows, K): several rows for each resident CTA at each depth of the ring and number of pieces
+    (9001, 200), (5003, 2048), (4001, 3592), (3001, 10000), (2003, 16384), (4099, 1000),
+]
+
+
+@pytest.mark.parametrize("xt,rt", [("bf16", "bf16"), ("f32", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", None),
+                                   ("bf16", None)])
+@pytest.mark.parametrize("M,K", NORM_LOOPS)
+def test_rmsnorm_rows_one_after_another(hxq, M, K, xt, rt):
+    """CTAs that take many rows: each row against float64, with the sum in place of the residual. A few rows among
+    them need their mean in 64 bits (from shared memory, while later rows arrive), are zeros, or hold a NaN."""
+    import torch
+    x = randn(M + K, M, K).to(dtype(xt))
+    x[5::611] *= 1e25
+    x[11::613] *= 1e-30
+    x[17::617] = 0
+    x[23::619, K // 2] = float("nan")
+    res = randn(M + K + 1, M, K, scale=2.0).to(dtype(rt)) if rt else None
+    if rt:
+        res[5::611] *= 1e25
+        res[11::613] *= 1e-30
+        res[17::617] = 0
+    w = 1 + randn(M + K + 2, K, scale=0.2)
+    t = x if res is None else (x.float() + res.float()).to(res.dtype)
+    own = res.clone() if rt else None
+    q, s, y, total = hxq.rmsnorm(x, w, 1e-6, residual=own, sum_out=own, want="qy")
+    if rt:
+        assert torch.equal(total.nan_to_num(7.0), t.nan_to_num(7.0)) and torch.equal(total.isnan(), t.isnan())
+    d = t.double()
+    h = d / torch.sqrt((d * d).mean(1, keepdim=True) + 1e-6) * w.double()
+    # y of every row, on the GPU
+    ok = (y.double() - h).abs() <= (2.0 ** -8 + DELTA) * h.abs() + 2.0 ** -133
+    assert (ok | (h.isnan() & y.isnan())).all()
+    # scales of every block: the smallest power of two with max <= 448 s
+    kb = -(-K // 128)
+    a = torch.zeros(M, kb * 128, dtype=torch.float64, device="cuda")
+    a[:, :K] = h.abs().nan_to_num(0.0)
+    a = a.view(M, kb, 128).amax(2)
+    m, e = torch.frexp(a / 448)
+    want = torch.where(a == 0, 1.0, torch.ldexp(torch.ones_like(m), (e - (m == 0.5).int()).clamp(-126, 120)))
+    assert torch.equal(s.double(), want)
+    # every byte within the rounding of h to e4m3: half a step of 2^-3 of its binade, 2^-10 at the least
+    v = h / want.repeat_interleave(128, 1)[:, :K]
+    got = q[:, :K].double()
+    step = torch.ldexp(torch.ones_like(v), (torch.frexp(v.abs().nan_to_num(1.0))[1] - 1).clamp(min=-6) - 3)
+    assert ((got - v).abs() <= step / 2 + DELTA * v.abs()).logical_or(v.isnan() & got.isnan()).all()
+    assert not q.view(torch.uint8)[:, K:].any()
+    # and some rows byte by byte, the special ones and the last ones among them
+    rows = [0, 1, 5, 11, 17, 5 + 611, 11 + 613, 17 + 617, M // 2, M - 2, M - 1]
+    check_bytes(q[rows], s[rows], h[rows].cpu().numpy(), K, DELTA)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("E,N,K", [(1, 6000, 4000), (3, 1500, 4104), (1, 128, 131072), (1, 6000, 1001)])
+def test_encode_blocks_one_after_another(hxq, E, N, K, dt):
+    """Five and more blocks for each SM: slots that are filled again. Every byte against float64, with blocks of
+    zeros, NaN, infinities and numbers below fp32's normal ones among them."""
+    import torch
+    W = randn(N + K, E, N, K, scale=0.02)
+    W *= torch.exp2(torch.randint(-20, 20, (E, -(-N // 128), -(-K // 128)), device="cuda").float()) \
+        .repeat_interleave(128, 1)[:, :N].repeat_interleave(128, 2)[:, :, :K]
+    W[0, 0, 130] = float("nan")
+    W[0, -1, -1] = float("inf")
+    W[-1, 50, 300] = -float("inf")
+    W[0, :128, 384:512] = 0
+    W[0, :128, 512:640] = W[0, :128, 512:640].sign() * 1e-41
+    W = W.to(dtype(dt))
+    q, s = hxq.fp8_encode(W)
+    for e in range(E):
+        nb, kb = -(-N // 128), -(-K // 128)
+        a = torch.zeros(nb * 128, kb * 128, dtype=torch.float64, device="cuda")
+        a[:N, :K] = W[e].double().abs().nan_to_num(0.0, posinf=3.402823466e38)
+        a = a.view(nb, 128, kb, 128).amax((1, 3))
+        m, x = torch.frexp(a / 448)
+        want = torch.where(a == 0, 1.0, torch.ldexp(torch.ones_like(m), (x - (m == 0.5).int()).clamp(-126, 120)))
+        assert torch.equal(s[e].double(), want)
+        full = want.repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+        v = W[e].double() / full
+        v[v.isinf()] = float("nan")
+        # torch rounds fp32 to e4m3 to nearest even; v is exact in fp32 unless below its normal numbers, where both are 0
+        ref = v.float().to(torch.float8_e4m3fn).float()
+        got = q[e].float()
+        assert torch.equal(got.nan_to_num(999.0), ref.nan_to_num(999.0)) and torch.equal(got.isnan(), ref.isnan())
+
+
+@pytest.mark.parametrize("counts,N,K", [([2] * 8, 2048, 14336), ([0, 5, 1, 0, 7, 1, 1, 1], 2048, 14336),
+                                        ([20] * 8, 1024, 8192), ([40] * 4, 2048, 8192), ([60, 3, 64, 50], 1500, 8200)],
+                         ids=lambda v: str(v)[:20])
+@pytest.mark.parametrize("out", [0, 1])
+def test_clusters_with_several_units(hxq, counts, N, K, out):
+    """Clusters that exchange sums for one unit after another: the receiving rows are used again."""
+    import torch
+    E, M = len(counts), sum(counts)
+    xq, xs = make_activation(M, M, K)
+    wq, ws = make_weights(N, E, N, K)
+    lin = hxq.Fp8Linear(wq, ws)
+    y = lin.forward_grouped(xq, xs, offsets_of(counts), out_dtype=out)
+    at = 0
+    for e, n in enumerate(counts):
+        if n:
+            check_product(y[at:at + n], dense_x(xq[at:at + n], xs[at:at + n], K), dense_w(wq[e], ws[e]), None, f"expert {e}")
+        at += n
+    for _ in range(5):
+        assert torch.equal(lin.forward_grouped(xq, xs, offsets_of(counts), out_dtype=out), y)
+    lin.check()
+
+
+@pytest.mark.parametrize("M", [16, 30, 64])
+@pytest.mark.parametrize("out", [0, 1])
+def test_clusters_with_two_units_of_one_layer(hxq, M, out):
+    """86 tiles for some 45 clusters of three."""
+    import torch
+    N, K = 11008, 8192
+    xq, xs = make_activation(M, M, K)
+    wq, ws = make_weights(N, 1, N, K)
+    bias = randn(4, N)
+    lin = hxq.Fp8Linear(wq[0], ws[0])
+    y = lin.forward(xq, xs, bias=bias, out_dtype=out)
+    check_product(y, dense_x(xq, xs, K), dense_w(wq[0], ws[0]), bias)
+    for _ in range(5):
+        assert torch.equal(lin.forward(xq, xs, bias=bias, out_dtype=out), y)
+    lin.check()
+
+
+# (512 x 2048 x 2048: 16 units on 74 pairs, pieces of 64 features; 1100 x 2048: 40, pieces of 128)
+@pytest.mark.parametrize("M,N,K", [(512, 2048, 2048), (512, 1920, 2048), (300, 2048, 2048), (512, 2008, 2048),
+                                   (1100, 2048, 2048), (290, 2177, 2048), (512, 2500, 2048)])
+def test_units_cut_into_pieces(hxq, M, N, K):
+    """The last round's units by pieces of 64 or 128 features: stores narrower than a box of 128 bytes, odd tiles and
+    ends of rows among them."""
+    import torch
+    xq, xs = make_activation(M, M, K)
+    wq, ws = make_weights(N, 1, N, K)
+    bias = randn(3, N)
+    lin = hxq.Fp8Linear(wq[0], ws[0])
+    x, w = dense_x(xq, xs, K), dense_w(wq[0], ws[0])
+    for out in (hxq.HXQ_OUT_F32, hxq.HXQ_OUT_BF16):
+        for b in (None, bias):
+            buf = torch.full((M + 2, N), 7.0, dtype=torch.bfloat16 if out else torch.float32, device="cuda")
+            y = lin.forward(xq, xs, bias=b, out_dtype=out, y=buf[1:M + 1])
+            check_product(y, x, w, b, f"out={out}")
+            assert (buf[0] == 7).all() and (buf[-1] == 7).all()
+    lin.check()
+
+
+FIRST_CALLS_CAPTURED = """
+import torch
+import vq_compressed_linear_b200 as hxq
+W, W2 = torch.randn(640, 512, device="cuda"), torch.randn(2, 640, 512, device="cuda")
+w, off = torch.ones(512, device="cuda"), torch.tensor([0, 1, 1], dtype=torch.int32, device="cuda")
+lin, ex = hxq.Fp8Linear(*hxq.fp8_encode(W)), hxq.Fp8Linear(*hxq.fp8_encode(W2))
+xs = [torch.randn(m, 512, device="cuda").bfloat16() for m in (1, 20, 60, 600)]
+
+def run():
+    out = []
+    for x in xs:
+        q, s, y, t = hxq.rmsnorm(x, w, 1e-6, residual=x, want="qy")
+        out += [lin(q, s), y, t, lin(*hxq.fp8_quantize(x)), lin(*hxq.fp8_swiglu(torch.cat([x, x], 1)))]
+        y = torch.zeros(x.shape[0], 640, device="cuda")
+        out.append(ex.forward_grouped(*hxq.fp8_quantize(x.float()), off, y=y))
+    return out
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+lin.check()
+ex.check()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+print("equal")
+"""
+
+
+def test_first_calls_of_a_process_captured():
+    """What a call looks up or sets once (kernel attributes, residency) is no harm to a capture that it falls into."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "equal", r.stderr[-2000:]
