@@ -346,3 +346,35 @@ def test_first_calls_of_a_process_captured():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=root, capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip() == "equal", r.stderr[-2000:]
+
+
+def test_longest_rows(hxq):
+    """One row of 2^31 - 1 columns through the norm, the quantiser and the encoder: both ends and the middle."""
+    import torch
+    K = 2**31 - 1
+    x = torch.empty(1, K, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    x[0, K - 128:] *= 1000  # (the last block's scale is its own)
+    ss = sum(x[0, i:i + 2**27].double().square().sum() for i in range(0, K, 2**27))
+    parts = [slice(0, 1024), slice(2**30, 2**30 + 1024), slice(K // 128 * 128 - 1024, K)]
+
+    def check(q, s, f, delta):
+        for p in parts:
+            h = f(x[:, p].double())
+            n = h.shape[1]
+            at = slice(p.start // 128, p.start // 128 + -(-n // 128))
+            check_bytes(q[:, p.start:p.start + -(-n // 16) * 16], s[:, at], h.cpu().numpy(), n, delta)
+
+    q, s = hxq.fp8_quantize(x)
+    assert q.shape == (1, 2**31) and codes(q[:, -16:])[0, 15] == 0
+    check(q, s, lambda v: v, 0.0)
+    q, s, y, _ = hxq.rmsnorm(x, None, 0.0, want="qy")
+    root = torch.sqrt(ss / K)
+    check(q, s, lambda v: v / root, DELTA)
+    for p in parts:
+        check_y(y[:, p], (x[:, p].double() / root).cpu().numpy())
+    del q, s, y
+    q, s = hxq.fp8_encode(x)
+    for p in parts:
+        n = min(p.stop, K) - p.start
+        at = slice(p.start // 128, p.start // 128 + -(-n // 128))
+        check_bytes(q[:, p], s[:, at], x[:, p].double().cpu().numpy(), n, rows=128)

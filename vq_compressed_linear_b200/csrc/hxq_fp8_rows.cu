@@ -31,6 +31,9 @@ namespace {
 constexpr int kVec = 8;                        // elements per thread and block of 128: 16 lanes share a block
 constexpr int kLanesPerBlock = kFp8Block / kVec;
 
+// Pieces of kVec columns in a row of any length below 2^31.
+__host__ __device__ inline int pieces_of(int cols) { return cols / kVec + (cols % kVec != 0); }
+
 // 8 elements from p (fp32 or bf16) as floats; VEC: p is 16-byte aligned and
 // all 8 exist, else element by element with zeros past n.
 template <bool BF16, bool VEC>
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs
     // the row's mean of squares in 64 bits, by one warp from shared memory
     auto mean64 = [&]() {
       double s64 = 0.0;
-      for (int k = tid & 31; k < (cols + kVec - 1) / kVec; k += 32) {
+      for (int k = tid & 31; k < pieces_of(cols); k += 32) {
         float v[8];
         uint4 w;
         load_t(d, k / T, k % T, v, w);
@@ -570,7 +573,7 @@ template <bool XBF16, bool RBF16, bool VEC>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
   const int64_t row = blockIdx.x;
   const int T = blockDim.x, tid = threadIdx.x, cols = a.cols;
-  const int iters = ((cols + kVec - 1) / kVec + T - 1) / T;
+  const int iters = (pieces_of(cols) + T - 1) / T;
   __shared__ double part[32];
   pdl_launch_dependents();
   pdl_wait();
@@ -962,10 +965,11 @@ __global__ void __launch_bounds__(256) encode_any_kernel(const void* w, int N, i
   const int64_t blk = blockIdx.x, en = blk / kb, e = en / nb;
   const int c0 = (int)(blk - en * kb) * kFp8Block, rb = (int)(en - e * nb);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nc = min(kFp8Block, K - c0);  // (c0 + 128 may be 2^31)
   auto each = [&](auto f) {
     for (int r = warp; r < min(kFp8Block, N - rb * kFp8Block); r += 8)
-      for (int c = c0 + lane; c < min(c0 + kFp8Block, K); c += 32) {
-        const int64_t at = (e * N + rb * kFp8Block + r) * (int64_t)K + c;
+      for (int c = lane; c < nc; c += 32) {
+        const int64_t at = (e * N + rb * kFp8Block + r) * (int64_t)K + c0 + c;
         f(at, BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(w)[at] << 16)
                    : static_cast<const float*>(w)[at]);
       }
@@ -1067,7 +1071,7 @@ template <bool XB, bool RB, bool VEC>
 cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t s) {
   // `pieces` of 8 columns per thread, `depth` rows in shared memory, as many
   // CTAs as fit at once
-  const int ch = (a.cols + kVec - 1) / kVec;
+  const int ch = pieces_of(a.cols);
   auto go = [&](auto kern, int t, int pieces, int depth) -> cudaError_t {
     t = (t + 31) / 32 * 32;
     const size_t smem = (size_t)depth * pieces * t * ((XB ? 16 : 32) + (a.res ? RB ? 16 : 32 : 0));
