@@ -378,3 +378,72 @@ def test_longest_rows(hxq):
         n = min(p.stop, K) - p.start
         at = slice(p.start // 128, p.start // 128 + -(-n // 128))
         check_bytes(q[:, p], s[:, at], x[:, p].double().cpu().numpy(), n, rows=128)
+
+
+# ---- forms that the documentation allows ------------------------------------------------
+
+@pytest.mark.parametrize("K", [250, 2048, 5000, 33000])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_rmsnorm_sum_in_place_of_x(hxq, dt, K):
+    """sum may be x; x and the residual may be one tensor."""
+    import torch
+    x, res = randn(1, 700, K).to(dtype(dt)), randn(2, 700, K).to(dtype(dt))
+    q, s, y, t = hxq.rmsnorm(x, None, 1e-6, residual=res, want="qy")
+    own = x.clone()
+    q1, s1, y1, t1 = hxq.rmsnorm(own, None, 1e-6, residual=res, sum_out=own, want="qy")
+    assert t1 is own and torch.equal(own, t) and torch.equal(y1, y) and torch.equal(s1, s)
+    assert torch.equal(q1.view(torch.uint8), q.view(torch.uint8))
+    own = x.clone()
+    q2, s2, _, _ = hxq.rmsnorm(own, None, 1e-6, residual=own, sum_out=own)
+    q3, s3, _, _ = hxq.rmsnorm(x, None, 1e-6, residual=x)
+    assert torch.equal(own, (x.float() * 2).to(x.dtype))
+    assert torch.equal(q2.view(torch.uint8), q3.view(torch.uint8)) and torch.equal(s2, s3)
+
+
+def test_weights_from_the_host_and_other_layouts(hxq):
+    """Pageable, pinned, bytes, transposed and sliced weights give what their plain copy gives."""
+    import torch
+    N, K, M = 260, 700, 33
+    xq, xs = make_activation(1, M, K)
+    wq, ws = make_weights(2, 3, N, K)
+    want = hxq.Fp8Linear(wq[1], ws[1]).forward(xq, xs)
+    off = offsets_of([10, 0, 23])
+    want_e = hxq.Fp8Linear(wq, ws).forward_grouped(xq, xs, off)
+    wide = torch.zeros(N, K + 9, dtype=torch.uint8, device="cuda")
+    wide[:, 5:5 + K] = wq[1].view(torch.uint8)
+    for W, S in ((wq[1].cpu(), ws[1].cpu()), (wq[1].view(torch.uint8), ws[1].cpu().pin_memory()),
+                 (wq[1].view(torch.uint8).cpu().pin_memory(), ws[1]), (wide[:, 5:5 + K], ws[1]),
+                 (wq[1].view(torch.uint8).t().contiguous().t(), ws[1].t().contiguous().t())):
+        assert torch.equal(hxq.Fp8Linear(W, S).forward(xq, xs), want)
+    assert torch.equal(hxq.Fp8Linear(wq.cpu(), ws.cpu()).forward_grouped(xq.view(torch.uint8), xs, off), want_e)
+
+
+@pytest.mark.parametrize("M", [1, 30, 600])
+def test_outputs_and_inputs_at_odd_addresses(hxq, M):
+    """y, bias, scales and offsets aligned as their elements only."""
+    import torch
+    N, K, E = 1024, 640, 3
+    xq, xs = make_activation(1, M, K)
+    wq, ws = make_weights(2, E, N, K)
+    bias = randn(3, E, N)
+    counts = [M // 3, 0, M - M // 3]
+    off = offsets_of(counts)
+    one, ex = hxq.Fp8Linear(wq[0], ws[0]), hxq.Fp8Linear(wq, ws)
+    for out, dt in ((hxq.HXQ_OUT_F32, torch.float32), (hxq.HXQ_OUT_BF16, torch.bfloat16)):
+        buf = torch.full((M * N + 3,), 7.0, dtype=dt, device="cuda")
+        y = buf[1:M * N + 1].view(M, N)
+        one.forward(xq, unaligned(xs), bias=unaligned(bias[0]), out_dtype=out, y=y)
+        check_product(y, dense_x(xq, xs, K), dense_w(wq[0], ws[0]), bias[0])
+        ex.forward_grouped(xq, unaligned(xs), unaligned(off), bias=unaligned(bias), out_dtype=out, y=y)
+        at = 0
+        for e, n in enumerate(counts):
+            if n:
+                r = slice(at, at + n)
+                check_product(y[r], dense_x(xq[r], xs[r], K), dense_w(wq[e], ws[e]), bias[e])
+            at += n
+        assert buf[0] == 7 and (buf[M * N + 1:] == 7).all()
+    x = randn(5, M, K)
+    for f in (lambda q, s: hxq.fp8_quantize(x, q=q, scales=s), lambda q, s: hxq.rmsnorm(x, q=q, scales=s)[:2]):
+        a = f(None, None)
+        b = f(None, unaligned(a[1]))
+        assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
