@@ -360,7 +360,11 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
 
 // With eps 0 and a root mean square below 2.9e-39 (a row of subnormal numbers)
 // 1 / root leaves fp32: root() is infinite. Such a row's t are taken times kLift
-// (exact) and its factor divided by it. A row of zeros keeps 0 / 0.
+// (exact) and its factor divided by it. A row of zeros keeps 0 / 0. And where
+// the factor is not finite (a NaN in the row, 0 / 0), 0 times it is no padding.
+// Neither can happen with an eps and rows of whole 16 bytes: the forms of the
+// kernels for those (CAREFUL false) have none of the checks, which cost fp32 rows
+// 3 to 9 % (8192 x 2048 with both outputs 42.6 us without, 46.5 with).
 constexpr double kLift = 0x1p64;
 __device__ __forceinline__ float lifted_root(double mean) { return (float)(1.0 / (sqrt(mean) * kLift)); }
 
@@ -368,7 +372,7 @@ __device__ __forceinline__ float lifted_root(double mean) { return (float)(1.0 /
 // c .., lifted if the row is), their weights and the row's statistics: h = t
 // rstd g as bf16 and / or 8 bits. mean64(): the mean of squares (plus eps) in 64 bits, asked for by a
 // whole warp and only where it decides a scale.
-template <bool VEC, typename Mean64>
+template <bool VEC, bool CAREFUL, typename Mean64>
 __device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t ld, int kb, int c,
                                          const float (&t)[8], const float (&g)[8], float rstd, Mean64 mean64) {
   const int n = a.cols - c;
@@ -390,7 +394,7 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t
       }
       if (__any_sync(0xffffffffu, unsure)) {
         double r = 1.0 / sqrt(mean64());
-        if (isinf((float)r)) r /= kLift;
+        if (CAREFUL && isinf((float)r)) r /= kLift;
         double m = 0.0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -404,8 +408,10 @@ __device__ __forceinline__ void norm_out(const NormArgs& a, int64_t row, int64_t
       }
     }
     if (isinf(amax)) no_infinities(h);
+    if (CAREFUL) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = j < n ? h[j] : 0.f;  // (the row's padding, where the root is not finite)
+      for (int j = 0; j < 8; ++j) h[j] = j < n ? h[j] : 0.f;
+    }
     put8(a.q + row * ld, ld, c, h, inv);
     const int b = c / kFp8Block;
     if ((threadIdx.x & (kLanesPerBlock - 1)) == 0 && b < kb) a.scales[row * kb + b] = s;
@@ -428,7 +434,7 @@ __device__ __forceinline__ float root(double mean) {
 // Sums are fp32 in a warp (9 roundings deep at most) and 64 bits across warps;
 // other 64 bits come on demand. 8192 x 2048 fp32 rows with both
 // outputs: 43 us, 5.9 TB/s.
-template <bool XBF16, bool RBF16, int NCH, int D>
+template <bool XBF16, bool RBF16, int NCH, int D, bool CAREFUL>
 __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs a, int64_t rows) {
   constexpr int XB = XBF16 ? 16 : 32, RB = RBF16 ? 16 : 32;  // bytes of 8 elements
   const int T = blockDim.x, tid = threadIdx.x, cols = a.cols;
@@ -549,7 +555,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs
     if (!(mean < 1e37 && mean > 1e-30)) {  // squares beyond the range of fp32
       const double m = mean64();
       rstd = root(m);
-      if (isinf(rstd)) {
+      if (CAREFUL && isinf(rstd)) {
         rstd = lifted_root(m);
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
@@ -558,7 +564,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs
       }
     }
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) norm_out<true>(a, row, ld, kb, col(i), t[i], g[i], rstd, mean64);
+    for (int i = 0; i < NCH; ++i) norm_out<true, CAREFUL>(a, row, ld, kb, col(i), t[i], g[i], rstd, mean64);
     if (D == 1) {
       __syncthreads();  // every warp is done with the slot
       fetch(0);
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(NCH == 1 ? 256 : 1024) rmsnorm_kernel(NormArgs
 
 // Rows longer than that, or not of whole 16-byte pieces: one CTA per row, the
 // row read twice, the sum in 64 bits.
-template <bool XBF16, bool RBF16, bool VEC>
+template <bool XBF16, bool RBF16, bool VEC, bool CAREFUL>
 __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
   const int64_t row = blockIdx.x;
   const int T = blockDim.x, tid = threadIdx.x, cols = a.cols;
@@ -602,7 +608,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
   for (int w = 0; w < T / 32; ++w) ss += part[w];
   const double mean = ss / cols + (double)a.eps;
   float rstd = root(mean);
-  const bool lift = isinf(rstd);
+  const bool lift = CAREFUL && isinf(rstd);
   if (lift) rstd = lifted_root(mean);
   for (int i = 0; i < iters; ++i) {
     const int c = (i * T + tid) * kVec;
@@ -619,7 +625,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_long_kernel(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) g[j] = 1.f;
     }
-    norm_out<VEC>(a, row, fp8_ld(cols), fp8_blocks(cols), c, t, g, rstd, [&]() { return mean; });
+    norm_out<VEC, CAREFUL>(a, row, fp8_ld(cols), fp8_blocks(cols), c, t, g, rstd, [&]() { return mean; });
   }
 }
 
@@ -655,6 +661,7 @@ __device__ __forceinline__ void load_sum(const uint8_t* xs, const uint8_t* rs, b
 // (fp32 rows are better off in rmsnorm_kernel, 83 us for 8192 x 3584 against
 // 95 here: they are twice as long in shared memory, and fewer fit.)
 constexpr int kPieces = 4, kBf16Slots = 3;
+template <bool CAREFUL>
 __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t rows) {
   constexpr int D = kBf16Slots, P = kPieces, L = kLanesPerBlock / P, kStep = L * kVec;  // threads of a block, columns from piece to piece
   const int T = blockDim.x, tid = threadIdx.x, cols = a.cols;
@@ -753,7 +760,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
     if (!(mean < 1e37 && mean > 1e-30)) {  // squares beyond the range of fp32
       const double m = mean64();
       rstd = root(m);
-      if (isinf(rstd)) {
+      if (CAREFUL && isinf(rstd)) {
         rstd = lifted_root(m);
 #pragma unroll
         for (int k = 0; k < P; ++k)
@@ -818,7 +825,7 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
             if (pass == 0) continue;
             if (a.y && far) store8<true, true>(a.y, row * cols + c, cols - c, v);
             if (isinf((float)m)) no_infinities(v);
-            if (c >= cols) {  // the row's padding, where the root is not finite
+            if (CAREFUL && c >= cols) {
 #pragma unroll
               for (int j = 0; j < 8; ++j) v[j] = 0.f;
             }
@@ -848,7 +855,8 @@ __global__ void __launch_bounds__(512) rmsnorm_bf16_kernel(NormArgs a, int64_t r
       const float s = fp8_scale(amax, &inv);
       uint8_t* q = a.q + row * ld;
 #pragma unroll
-      for (int k = 0; k < P; ++k) put8(q, ld, c0 + kStep * k, t[k], c0 + kStep * k < cols ? rstd * inv : 0.f);
+      for (int k = 0; k < P; ++k)
+        put8(q, ld, c0 + kStep * k, t[k], !CAREFUL || c0 + kStep * k < cols ? rstd * inv : 0.f);
       if (tid % L == 0 && blk < kb) a.scales[row * kb + blk] = s;
     }
     d = d + 1 == D ? 0 : d + 1;
@@ -1067,8 +1075,8 @@ cudaError_t resident(const void* kern, int t, size_t smem, int64_t* ctas) {
   return cudaSuccess;
 }
 
-template <bool XB, bool RB, bool VEC>
-cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t s) {
+template <bool XB, bool RB, bool VEC, bool CAREFUL>
+cudaError_t launch_norm_as(const NormArgs& a, int64_t rows, cudaStream_t s) {
   // `pieces` of 8 columns per thread, `depth` rows in shared memory, as many
   // CTAs as fit at once
   const int ch = pieces_of(a.cols);
@@ -1082,14 +1090,19 @@ cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t s) {
   };
   if constexpr (VEC && XB && RB) {
     const int t = fp8_blocks(a.cols) * (kLanesPerBlock / kPieces);
-    if (a.cols <= 16384) return go(rmsnorm_bf16_kernel, t, kPieces, kBf16Slots);
+    if (a.cols <= 16384) return go(rmsnorm_bf16_kernel<CAREFUL>, t, kPieces, kBf16Slots);
   } else if constexpr (VEC) {
-    if (ch <= 256) return go(rmsnorm_kernel<XB, RB, 1, 4>, ch, 1, 4);
-    if (ch <= 1024) return go(rmsnorm_kernel<XB, RB, 2, 3>, (ch + 1) / 2, 2, 3);
-    if (ch <= 2048) return go(rmsnorm_kernel<XB, RB, 2, 1>, (ch + 1) / 2, 2, 1);
+    if (ch <= 256) return go(rmsnorm_kernel<XB, RB, 1, 4, CAREFUL>, ch, 1, 4);
+    if (ch <= 1024) return go(rmsnorm_kernel<XB, RB, 2, 3, CAREFUL>, (ch + 1) / 2, 2, 3);
+    if (ch <= 2048) return go(rmsnorm_kernel<XB, RB, 2, 1, CAREFUL>, (ch + 1) / 2, 2, 1);
   }
-  return launch_pdl(rmsnorm_long_kernel<XB, RB, VEC>, (unsigned)rows, (unsigned)std::min(1024, (ch + 31) / 32 * 32), 0, s,
-                    a);
+  return launch_pdl(rmsnorm_long_kernel<XB, RB, VEC, CAREFUL>, (unsigned)rows,
+                    (unsigned)std::min(1024, (ch + 31) / 32 * 32), 0, s, a);
+}
+template <bool XB, bool RB, bool VEC>
+cudaError_t launch_norm(const NormArgs& a, int64_t rows, cudaStream_t s) {
+  return a.eps == 0.f || a.cols % 16 ? launch_norm_as<XB, RB, VEC, true>(a, rows, s)
+                                     : launch_norm_as<XB, RB, VEC, false>(a, rows, s);
 }
 
 }  // namespace
