@@ -426,8 +426,9 @@ int hxq_fp8_quantize(const void* x, int x_type, int64_t rows, int cols, uint8_t*
  * The gated activation between an MLP's products, as an 8-bit activation:
  * gate_up [rows][2 * cols] holds gate in its first cols columns and up in the
  * others; q and scales [rows][cols] receive gate / (1 + exp(-gate)) * up,
- * formed in fp32 (a value beyond its range counts as infinite). Errors as
- * hxq_fp8_quantize.
+ * formed in fp32 (a value beyond its range counts as infinite). Blocks that
+ * fp32 cannot settle are formed in 64 bits, blocks of zeros among them: rows of
+ * zeros take some ten times as long as others. Errors as hxq_fp8_quantize.
  */
 int hxq_fp8_swiglu(const void* gate_up, int type, int64_t rows, int cols, uint8_t* q, float* scales,
                    void* stream);
@@ -459,8 +460,11 @@ int hxq_fp8_encode(const void* W, int type, int n_experts, int N, int K, uint8_t
  *  q, scales      receive h as an 8-bit activation (what hxq_fp8_forward
  *                 reads; from the fp32 h), or both NULL
  *
- * h is formed in fp32; the mean of squares, and every scale that the rounding
- * of h could decide, in 64 bits. Returns HXQ_EINVAL for a NULL x, neither y
+ * h is formed in fp32, within 16 2^-24 of its value. The mean of squares is a
+ * sum in fp32 within a warp and in 64 bits across warps for aligned rows of up to
+ * 16384 columns (at most 22 roundings deep, which the root halves), all in 64
+ * bits for others and where fp32's range ends. A scale that these roundings
+ * could decide is settled in 64 bits. Returns HXQ_EINVAL for a NULL x, neither y
  * nor q, one of q and scales without the other, a sum without a residual,
  * unknown types, a negative, infinite or NaN eps, sizes as hxq_fp8_quantize,
  * misaligned or unreachable outputs; HXQ_ECUDA if the launch fails.

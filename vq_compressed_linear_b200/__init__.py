@@ -467,7 +467,9 @@ def encode(W, mode, codebook, threshold, max_sidecar=None, stream=None):
 # contiguity and device. A mismatch raises HXQError with HXQ_EINVAL. A call
 # runs on the current torch stream, or on `stream` as if it were that. These
 # wrappers sit in the path of a decode step: they call the library directly,
-# take outputs that exist already, and build no message unless they raise.
+# take outputs that exist already, and build no message unless they raise. None
+# of these operators has a backward pass: results carry no gradient, whatever
+# the inputs require.
 
 class _Torch:
     """What the wrappers use of torch, looked up once (importing this module
@@ -583,7 +585,8 @@ def fp8_encode(W, q=None, scales=None, stream=None):
 def rmsnorm(x, weight=None, eps=1e-6, residual=None, sum_out=None, y=None, q=None, scales=None, want=None,
             stream=None):
     """t = x + residual (rounded to the residual's type), then
-    h = t / sqrt(mean(t^2) + eps) * weight per row of x [M, K].
+    h = t / sqrt(mean(t^2) + eps) * weight per row of x [M, K]; weight is
+    float32 [K].
 
     want: "q" for h as an 8-bit activation (what Fp8Linear takes), "y" for h
     as bfloat16 (what HelixLinear takes), "qy" for both; by default what is

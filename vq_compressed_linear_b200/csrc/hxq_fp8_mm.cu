@@ -240,7 +240,7 @@ struct Walk {
 // adds the columns it owns in rank order: bitwise repeatable, and no global
 // workspace. The scale of a column (its token's) comes from shared memory, four
 // columns a load, the tile's is one factor more.
-// 1 x 11008 x 2048 in 7.1 us (3.2 TB/s of weights), 29 x 2048 x 11008 in 9.3:
+// 1 x 11008 x 2048 in 7.0 us (3.2 TB/s of weights), 29 x 2048 x 11008 in 9.3:
 // the start (1 us to the first bytes), the last stage's way out and the
 // cluster's exchange (2 us) weigh as much as the 3.5 us that HBM needs.
 
