@@ -447,3 +447,17 @@ def test_outputs_and_inputs_at_odd_addresses(hxq, M):
         a = f(None, None)
         b = f(None, unaligned(a[1]))
         assert torch.equal(a[0].view(torch.uint8), b[0].view(torch.uint8)) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("K", [250, 2048, 5000, 33000])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_rmsnorm_residual_without_sum(hxq, dt, K):
+    """A NULL sum: the same norm, and neither x nor the residual changes."""
+    import torch
+    x, res = randn(1, 70, K).to(dtype(dt)), randn(2, 70, K).to(dtype(dt))
+    q, s, y, _ = hxq.rmsnorm(x, None, 1e-6, residual=res, want="qy")
+    q1, s1, y1 = torch.empty_like(q), torch.empty_like(s), torch.empty_like(y)
+    x0, res0, code = x.clone(), res.clone(), hxq.HXQ_TYPE_BF16 if dt == "bf16" else hxq.HXQ_TYPE_F32
+    hxq.hxq_rmsnorm(x, code, res, None, code, None, 1e-6, 70, K, y1, q1, s1)
+    assert torch.equal(q1.view(torch.uint8), q.view(torch.uint8)) and torch.equal(s1, s) and torch.equal(y1, y)
+    assert torch.equal(x, x0) and torch.equal(res, res0)
